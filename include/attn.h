@@ -313,6 +313,68 @@ int attn_proj_heads(const void* X, const void* W, const void* bias, int B, int n
 int attn_merge_proj(const void* O, const void* W_o, const void* bias, int B, int n, int H, int d,
                     int d_out, void* Y, void* stream);
 
+/*
+ * A key/value cache held in 4 bits (the KV cache of the transformer wiki page, at
+ * 17/64 of its bf16 bytes): writing into it, reading it back, and attention of a few
+ * query rows over it. Query heads may share cache heads: H is a multiple of H_kv, and
+ * query head h attends to cache head h / (H / H_kv).
+ *
+ * Quantisation. A group is 64 channels of one slot and head. With lo = min(0, min x)
+ * and hi = max(0, max x) over the group, the step s is (hi - lo) / 15 in fp32 rounded up
+ * to four significant bits, the zero u0 = rint(-lo / s) and the code
+ * u = min(max(rint(x / s) + u0, 0), 15) (rint: half to even); the value held is
+ * s (u - u0), which is exactly a bf16 number and at most s / 2 away from x. A group
+ * of zeros has s = 0. A group that holds a NaN, an infinity or a magnitude of 2^127 or more
+ * holds NaN in every channel.
+ *
+ * Memory. attn_cache_q4_size(...) bytes, 16-byte aligned, caller-owned:
+ * [B][H_kv][ceil(m / 64)] blocks of 34 (d_k + d_v) bytes, a block holding 64 slots:
+ * K codes (32 d_k bytes), K words (2 d_k), V codes (32 d_v), V words (2 d_v). The words
+ * are [slot][group] 16-bit: s as bf16 (its four low mantissa bits are 0) with u0 in
+ * those four bits, or 0x7FC0. The codes of slot k are a row of d / 2 bytes, low nibble
+ * first: K channel 64 q + 16 t + e is nibble e of the 8-byte unit t (d_k / 64) + q of row
+ * k ^ (bit 2 of k) (128 / d_k); V channel 64 q + 8 g + e is nibble e of the 4-byte unit
+ * g' (d_v / 64) + q of row k, g' = g, or at d_v = 128 g ^ 4 where bit 1 of k is set. The
+ * memory needs no initialisation: slots that no row may see are never used.
+ *
+ * attn_cache_q4_write quantises the rows K [B,H_kv,n,d_k] and V [B,H_kv,n,d_v] (bf16)
+ *   into it: row i of entry b goes to slot starts[b] + i for i < counts[b] (starts NULL:
+ *   0; counts NULL: n; device int32 [B]). Rows whose slot is outside [0, m) are
+ *   skipped, and every other slot keeps its bytes. For a decoding step starts holds the lengths
+ *   before the step, for a tail-padded batch of prompts counts their lengths.
+ * attn_cache_q4_read gives slots first .. first + n - 1 as bf16 K [B,H,n,d_k] and
+ *   V [B,H,n,d_v], exactly the values held, each cache head copied to its H / H_kv query
+ *   heads. Slots at or past key_lengths[b] (device int32 [B] or NULL: m) give 0, so that
+ *   K and V can go to attn_fwd under a mask with the same lengths.
+ * attn_decode_q4 is attn_decode over the cache: Q [B,H,n,d_k], O [B,H,n,d_v], LSE
+ *   [B,H,n], the masks, key_lengths and scale as there, slopes (device fp32 [H], or NULL for none) the
+ *   distance bias of attn_fwd_alibi. Up to 64 rows per cache head (n H / H_kv) take a
+ *   kernel that streams the cache once per 16 rows, its blocks dealt out evenly over the SMs as
+ *   the lengths on the device have them; more rows read the cache into the workspace
+ *   and run the tensor-core forward. The workspace (caller-owned, 256-byte aligned, at
+ *   least attn_decode_q4_workspace_size(...) bytes, contents on entry do not matter; 0
+ *   for short caches) belongs to one call at a time: calls that may overlap need one
+ *   each. O and LSE do not depend on the order in which CTAs run.
+ * All run on `stream` without synchronising. Return ATTN_OK or a negative
+ * attn_status_t (INVALID_ARG: H not a multiple of H_kv, a slot range outside the cache, a
+ * workspace that is too small, a null pointer; UNSUPPORTED: a head dim outside {64, 128},
+ * sizes beyond int range; MISALIGNED: K, V, Q, O or cache not 16-byte, the 32-bit arrays
+ * not 4-byte aligned); on error nothing is enqueued. m = 0 gives O = 0 and LSE = -inf.
+ */
+size_t attn_cache_q4_size(int B, int H_kv, int m, int d_k, int d_v);
+
+int attn_cache_q4_write(const void* K, const void* V, int B, int H_kv, int n, int m, int d_k, int d_v,
+                        const int32_t* starts, const int32_t* counts, void* cache, void* stream);
+
+int attn_cache_q4_read(const void* cache, int B, int H, int H_kv, int m, int first, int n, int d_k, int d_v,
+                       const int32_t* key_lengths, void* K, void* V, void* stream);
+
+size_t attn_decode_q4_workspace_size(int B, int H, int H_kv, int n, int m, int d_k, int d_v);
+
+int attn_decode_q4(const void* Q, const void* cache, int B, int H, int H_kv, int n, int m, int d_k, int d_v,
+                   int mask_kind, const int32_t* key_lengths, const float* slopes, float scale, void* O,
+                   float* LSE, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Human-readable name of a status code. */
 const char* attn_status_string(int status);
 

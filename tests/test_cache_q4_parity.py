@@ -1,0 +1,178 @@
+"""GPU parity of the cache held in 4 bits: the bytes that attn_cache_q4_write leaves and
+the values that attn_cache_q4_read gives, against the reference. Nothing is rounded
+beyond the format's definition, so every comparison is for equality."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import cache_q4
+from transformer_scaled_dot_03_gb300 import attn, build
+
+pytestmark = pytest.mark.gpu
+
+DIMS = [(64, 64), (128, 128), (64, 128), (128, 64)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    build.build()
+    return attn.load()
+
+
+def rows(seed, shape, spread=1.0):
+    """Normal values with an offset and a width per channel, some channels far wider."""
+    g = torch.Generator().manual_seed(seed)
+    width = torch.exp(0.5 * torch.randn(shape[-1], generator=g)) * spread
+    width[::29] *= 8
+    return (torch.randn(shape, generator=g) * width + 0.5 * spread * torch.randn(shape[-1], generator=g)).to(torch.bfloat16)
+
+
+def garbage(seed, B, H, m, dk, dv):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randint(0, 256, (B, H, -(-m // 64), 34 * (dk + dv)), generator=g, dtype=torch.uint8)
+
+
+def i32(v):
+    return None if v is None else torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def check_write(cache, K, V, starts, counts, m):
+    want = cache_q4.write(cache.numpy(), K, V, starts, counts, m)
+    guard = torch.full((4096,), 0x5A, dtype=torch.uint8, device="cuda")
+    buf = torch.cat([guard, cache.cuda().flatten(), guard])
+    got = buf[4096:-4096].view(cache.shape)
+    attn.cache_q4_write(got, K.cuda(), V.cuda(), i32(starts), i32(counts), m=m)
+    torch.cuda.synchronize()
+    assert torch.all(buf[:4096] == 0x5A) and torch.all(buf[-4096:] == 0x5A)
+    assert np.array_equal(got.cpu().numpy(), want)
+    return got
+
+
+@pytest.mark.parametrize("dk,dv", DIMS)
+@pytest.mark.parametrize("B,H,n,m", [(1, 1, 1, 1), (3, 2, 1, 200), (2, 3, 65, 65), (4, 2, 130, 321)])
+def test_write(dk, dv, B, H, n, m):
+    starts = [(37 * b) % (m - n + 1) for b in range(B)]
+    check_write(garbage(n + m, B, H, m, dk, dv), rows(1, (B, H, n, dk)), rows(2, (B, H, n, dv)), starts, None, m)
+
+
+@pytest.mark.parametrize("dk,dv", DIMS)
+def test_write_skips_rows_outside(dk, dv):
+    """Counts of zero and beyond n, starts before the cache, at its last slot and past it."""
+    B, n, m = 7, 20, 100
+    starts = [0, 90, -5, 99, 100, -50, 2 ** 31 - 10]
+    counts = [0, 20, 20, 50, 3, 20, 20]
+    check_write(garbage(3, B, 2, m, dk, dv), rows(4, (B, 2, n, dk)), rows(5, (B, 2, n, dv)), starts, counts, m)
+
+
+def test_write_without_positions_fills_from_the_first_slot():
+    check_write(garbage(6, 2, 2, 77, 64, 128), rows(7, (2, 2, 77, 64)), rows(8, (2, 2, 77, 128)), None, None, 77)
+
+
+def test_write_ties_extremes_and_bad_groups():
+    """Exact halves, groups of zeros, of one sign, subnormal, large, and ones that cannot be held."""
+    K = rows(9, (1, 1, 40, 128))
+    k = K[0, 0]
+    k[0] = 0
+    k[1, :64] = 0
+    k[2] = -3.0
+    k[3] = 2.5
+    k[4] = torch.arange(128).to(torch.bfloat16) / 2 % 15.5            # step 1 or so, halves
+    k[5, :64] = torch.tensor([15.0] + [i / 2 for i in range(31)] + [0.0] * 32)
+    k[6] = (rows(10, (128,)).double() * 2.0 ** -130).to(torch.bfloat16)
+    k[7] = (rows(11, (128,)).double() * 2.0 ** -121).to(torch.bfloat16)
+    k[8] = (rows(12, (128,)).clamp(-8, 8).double() * 2.0 ** 122).to(torch.bfloat16)
+    k[9, 0], k[10, 64], k[11, 127], k[12, 3] = float("nan"), float("inf"), -float("inf"), 2.0 ** 127
+    k[13] = torch.full((128,), 2.0 ** -133)                            # the smallest bf16
+    k[14, :64], k[14, 64:] = 2.0 ** 126.99, -(2.0 ** 126.99)
+    for i in range(15, 40):                                            # every step's mantissa, with halves
+        s = (8 + i % 8) * 2.0 ** (i % 5 - 2)
+        k[i] = ((torch.randint(-30, 31, (128,), generator=torch.Generator().manual_seed(i)) * s / 2).to(torch.bfloat16))
+    V = K.flip(2).contiguous()
+    got = check_write(garbage(13, 1, 1, 40, 128, 128), K, V, None, None, 40)
+    rk, rv = attn.cache_q4_read(got, 128, 40)
+    torch.cuda.synchronize()
+    assert np.array_equal(rk.double().cpu().numpy(), cache_q4.held(K), equal_nan=True)
+    assert np.array_equal(rv.double().cpu().numpy(), cache_q4.held(V), equal_nan=True)
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_write_many_rows(seed):
+    """Random rows of widely different magnitudes: the rounding and the step of each group."""
+    spread = [1e-20, 1e-3, 1.0, 1e20][seed]
+    check_write(garbage(20, 2, 2, 256, 128, 64), rows(21 + seed, (2, 2, 256, 128), spread),
+                rows(31 + seed, (2, 2, 256, 64), spread), None, None, 256)
+
+
+@pytest.mark.parametrize("dk,dv", DIMS)
+@pytest.mark.parametrize("group", [1, 3])
+@pytest.mark.parametrize("m,first,n,lens", [(1, 0, 1, None), (200, 0, 200, [200, 1, 0]), (321, 60, 130, [321, 100, 60]),
+                                            (130, 129, 1, [130, 129, 500]), (64, 10, 0, None)])
+def test_read(dk, dv, group, m, first, n, lens):
+    B, H = 3, 2
+    cache = cache_q4.write(garbage(40, B, H, m, dk, dv).numpy(), rows(41, (B, H, m, dk)), rows(42, (B, H, m, dv)), m=m)
+    wk, wv = cache_q4.read(cache, dk, m, lens)
+    guard = 4096
+    outs, bufs = [], []
+    for d in (dk, dv):
+        size = B * H * group * n * d
+        bufs.append(torch.full((size + 2 * guard,), -77.0, dtype=torch.bfloat16, device="cuda"))
+        outs.append(bufs[-1][guard:guard + size].view(B, H * group, n, d))
+    attn.cache_q4_read(torch.from_numpy(cache).cuda(), dk, m, i32(lens), H=H * group, first=first, n=n, K=outs[0], V=outs[1])
+    torch.cuda.synchronize()
+    for got, want, buf in zip(outs, (wk, wv), bufs):
+        assert torch.all(buf[:guard] == -77.0) and torch.all(buf[-guard:] == -77.0)
+        assert np.array_equal(got.double().cpu().numpy(), np.repeat(want[:, :, first:first + n], group, 1))
+
+
+def test_read_beyond_the_lengths_ignores_what_lies_there():
+    """Unwritten slots hold NaN steps: they read as 0 past the lengths."""
+    cache = torch.full((2, 2, 2, 34 * 128), 0xFF, dtype=torch.uint8, device="cuda")
+    K = rows(50, (2, 2, 100, 64)).cuda()
+    attn.cache_q4_write(cache, K, K, None, i32([10, 0]), m=100)
+    rk, rv = attn.cache_q4_read(cache, 64, 100, i32([10, 0]))
+    assert torch.all(rk[0, :, 10:] == 0) and torch.all(rk[1] == 0) and torch.equal(rk, rv)
+    assert torch.isfinite(rk).all()
+
+
+def test_offsets_beyond_32_bits():
+    """A cache of 4.9 GB: the last block of the last head lies past 2^32 bytes."""
+    B, H, m = 1, 40, 64 * 14000
+    cache = attn.cache_q4_empty(B, H, m, 128, 128)
+    assert cache.numel() > 1 << 32
+    cache.zero_()
+    K, V = rows(60, (B, H, 70, 128)), rows(61, (B, H, 70, 128))
+    attn.cache_q4_write(cache, K.cuda(), V.cuda(), i32([m - 70]))
+    rk, rv = attn.cache_q4_read(cache, 128, first=m - 100, n=100)
+    torch.cuda.synchronize()
+    assert torch.all(rk[:, :, :30] == 0)
+    assert np.array_equal(rk[:, :, 30:].double().cpu().numpy(), cache_q4.held(K))
+    assert np.array_equal(rv[:, :, 30:].double().cpu().numpy(), cache_q4.held(V))
+    # nothing else was written
+    assert int(cache.view(torch.int64).ne(0).sum()) == int(cache[:, :, -2:].contiguous().view(torch.int64).ne(0).sum())
+
+
+def test_step_by_step_in_a_captured_graph():
+    """Single tokens appended by a replayed graph whose positions advance on the device."""
+    B, H, m = 3, 2, 200
+    K, V = rows(70, (B, H, 150, 64)), rows(71, (B, H, 150, 128))
+    cache = garbage(72, B, H, m, 64, 128)
+    want = cache_q4.write(cache.numpy(), K, V, [0, 10, 50], None, m)
+    dev = cache.cuda()
+    k, v = K[:, :, :1].contiguous().cuda(), V[:, :, :1].contiguous().cuda()
+    starts = i32([0, 10, 50])
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        attn.cache_q4_write(dev, k, v, starts, m=m)
+        starts += 1
+    starts.copy_(i32([0, 10, 50]))
+    for i in range(150):
+        k.copy_(K[:, :, i:i + 1])
+        v.copy_(V[:, :, i:i + 1])
+        graph.replay()
+    torch.cuda.synchronize()
+    assert np.array_equal(dev.cpu().numpy(), want)

@@ -1,0 +1,348 @@
+"""GPU parity of the attention over a cache held in 4 bits (attn_decode_q4) against the
+fp64 oracle on the values that the cache holds.
+
+Tolerance. The values held and the fp16 operand of the query rows (a power of two
+times the bf16 value) are exact in the kernels. With w the softmax weights, v = s (u - u0):
+
+  - The kernel forms sum_j fp16(w_j s_j) u_j - sum_j w_j s_j u0_j: the rounding, half a step of
+    fp16 or 2^-11 relative, acts on the codes before the zero is taken out, so it moves
+    O by up to 2^-11 B with B = sum_j w_j s_j u_j, the oracle's output on s u.
+  - Both sums are held in fp32: a tensor-core addition loses up to 2^-23 of the sum (B), a
+    warp makes at most 256 of them here: 2^-15 B.
+  - A score is scale sum_c q_c s (u_c - u0) in fp32: per group four tensor-core additions of
+    q u, the zero taken out, the step, then the sum of the groups and the scale, at most 14
+    roundings of up to 2^-23 of sum_c |q_c| s u_c (or of what u0 takes out, no larger than s 15);
+    the distance bias adds one of its own size. With G = scale max (sum_c |q_c| s 15) + max bias:
+    e = 14 2^-23 G. A weight then moves by e w and the sum of the weights too: O by 2 e A, A = sum_j w_j |v_j|.
+  - O is rounded to bf16: 2^-8 of what was rounded.
+
+The many-row path rounds the weights to bf16 and multiplies them with v itself:
+2^-8 A in the place of the first two; its scores are sums of q k in fp32, within the same e.
+LSE: e, 2^-22 of its magnitude (the logarithm and two products), and 2^-20 for the sum of
+the exponentials (2^-22 each, fp32 additions)."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import cache_q4, oracle
+from transformer_scaled_dot_03_gb300 import attn, build, inputs
+
+from test_cache_q4_parity import DIMS, i32, rows
+
+pytestmark = pytest.mark.gpu
+
+GUARD = 4096
+MASKS = ["none", "causal", "key_padding", "causal_key_padding", "causal_cache"]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    build.build()
+    return attn.load()
+
+
+class Case:
+    """Q, and a cache whose slots past the lengths hold NaN steps."""
+
+    def __init__(self, B, H_kv, group, n, m, dk, dv, mask="none", lens=None, seed=0, slopes=False, q_scale=1.0,
+                 K=None, V=None):
+        self.B, self.H_kv, self.H, self.n, self.m, self.dk, self.dv, self.mask = B, H_kv, H_kv * group, n, m, dk, dv, mask
+        self.lens = lens
+        g = torch.Generator().manual_seed(seed)
+        self.Q = (torch.randn(B, self.H, n, dk, generator=g) * q_scale).to(torch.bfloat16)
+        K = rows(seed + 1, (B, H_kv, m, dk)) if K is None else K
+        V = rows(seed + 2, (B, H_kv, m, dv)) if V is None else V
+        blocks = -(-m // 64)
+        self.cache = torch.full((B, H_kv, blocks, 34 * (dk + dv)), 0xFF, dtype=torch.uint8, device="cuda")
+        attn.cache_q4_write(self.cache, K.cuda(), V.cuda(), None, i32(lens), m=m)
+        self.slopes = inputs.alibi_slopes(self.H) if slopes else None
+        held = np.ones((B, m), bool) if lens is None else np.arange(m) < np.array(lens)[:, None]
+        self.K = np.repeat(np.where(held[:, None, :, None], cache_q4.held(K), 0.0), group, 1)
+        self.V = np.repeat(np.where(held[:, None, :, None], cache_q4.held(V), 0.0), group, 1)
+        self.G = np.abs(self.Q.double().numpy()).sum(-1).max() * 15 * cache_q4.quantise(K)[1].max()
+        self.bias = float(self.slopes.max()) * (m + n) if slopes else 0.0
+        self.SU = np.repeat(np.where(held[:, None, :, None], cache_q4.coded(V), 0.0), group, 1)
+
+    def run(self, **kw):
+        size = self.B * self.H * self.n
+        ob = torch.full((size * self.dv + 2 * GUARD,), -77.0, dtype=torch.bfloat16, device="cuda")
+        lb = torch.full((size + 2 * GUARD,), -77.0, device="cuda")
+        O = ob[GUARD:-GUARD].view(self.B, self.H, self.n, self.dv)
+        L = lb[GUARD:-GUARD].view(self.B, self.H, self.n)
+        ws = attn.decode_q4_workspace_size(self.B, self.H, self.H_kv, self.n, self.m, self.dk, self.dv)
+        wb = torch.full((ws + 2 * 4096,), 0xFF, dtype=torch.uint8, device="cuda")      # NaN everywhere
+        lens = i32(self.lens) if self.mask in inputs.LENGTH_MASKS else None
+        attn.decode_q4(self.Q.cuda(), self.cache, self.mask, lens, m=self.m,
+                       slopes=None if self.slopes is None else self.slopes.cuda(), O=O, LSE=L,
+                       workspace=wb[4096:4096 + ws] if ws else None, **kw)
+        assert attn.device_status() == (attn.ATTN_OK, 0)
+        torch.cuda.synchronize()
+        for b, v in ((ob, -77.0), (lb, -77.0), (wb, 0xFF)):
+            edge = 4096
+            assert torch.all(b[:edge] == v) and torch.all(b[-edge:] == v), "written outside"
+        return O.double().cpu().numpy(), L.double().cpu().numpy()
+
+    def reference(self, scale=None, many=False):
+        """O, LSE and their tolerances (see above)."""
+        args = (self.mask, self.lens, scale)
+        kw = dict(slopes=self.slopes, threads=8)
+        Or, Lr = oracle.attn_fwd(self.Q, self.K, self.V, *args, **kw)
+        A, _ = oracle.attn_fwd(self.Q, self.K, np.abs(self.V), *args, **kw)
+        if many:
+            e = 2.0 ** -8 * A
+        else:
+            B, _ = oracle.attn_fwd(self.Q, self.K, self.SU, *args, **kw)
+            e = (2.0 ** -11 + 2.0 ** -15) * B
+        score = 14 * 2.0 ** -23 * (self.G * (self.dk ** -0.5 if scale is None else scale) + self.bias)
+        e = e + 2 * score * A
+        seen = np.isfinite(Lr)
+        lse_tol = score + 2.0 ** -22 * (np.abs(Lr[seen]).max() if seen.any() else 0) + 2.0 ** -20
+        return Or, Lr, e + 2.0 ** -8 * (np.abs(Or) + e), lse_tol
+
+    def check(self, label="", scale=None, many=False):
+        O, L = self.run(**({} if scale is None else {"scale": scale}))
+        Or, Lr, tol, lse_tol = self.reference(scale, many)
+        assert np.isfinite(O).all(), label
+        assert np.array_equal(np.isneginf(L), np.isneginf(Lr)) and not np.isnan(L).any(), label
+        over = np.abs(O - Or) - tol
+        worst = float(over.max())
+        assert worst <= 0, f"{label}: O off by {np.abs(O - Or).max():.3e}, {worst:.3e} past the tolerance"
+        seen = np.isfinite(Lr)
+        if seen.any():
+            off = float(np.abs(L[seen] - Lr[seen]).max())
+            assert off <= lse_tol, f"{label}: LSE off by {off:.3e} of {lse_tol:.3e}"
+        assert np.all(O[~seen] == 0), label
+
+
+@pytest.mark.parametrize("dk,dv", DIMS)
+@pytest.mark.parametrize("m", [1, 15, 64, 65, 700, 1025, 4097])
+def test_one_token(dk, dv, m):
+    Case(2, 3, 1, 1, m, dk, dv, seed=m).check(f"m={m}")
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128)])
+@pytest.mark.parametrize("group,n", [(1, 2), (1, 8), (2, 4), (3, 3), (8, 1), (5, 3), (16, 1), (4, 7), (8, 8)])
+def test_rows_that_share_a_cache_head(dk, dv, group, n):
+    """2 to 64 rows per cache head: one and several row tiles, whole and partial."""
+    for m in (200, 2000):
+        Case(2, 2, group, n, m, dk, dv, "causal", seed=group * n + m).check(f"group={group} n={n} m={m}")
+
+
+@pytest.mark.parametrize("dk,dv", DIMS)
+@pytest.mark.parametrize("mask", MASKS)
+@pytest.mark.parametrize("n", [1, 5])
+@pytest.mark.parametrize("m", [300, 1500])
+def test_masks_and_lengths(dk, dv, mask, n, m):
+    """Lengths full, 0, 1, fewer than the rows, on and next to a block's end."""
+    lens = [m, 0, 1, 3, 64, 65, 127, 128, m - 1] if mask in inputs.LENGTH_MASKS else None
+    Case(9, 2, 2, n, m, dk, dv, mask, lens, seed=m + n).check(f"{mask} n={n} m={m}")
+
+
+@pytest.mark.parametrize("mask", MASKS)
+@pytest.mark.parametrize("m", [130, 1300])
+def test_distance_bias(mask, m):
+    lens = [m, 0, 70, 5] if mask in inputs.LENGTH_MASKS else None
+    Case(4, 2, 3, 3, m, 64, 128, mask, lens, seed=m, slopes=True).check(f"{mask} m={m}")
+
+
+@pytest.mark.parametrize("n,m", [(3, 1), (8, 5), (5, 5), (64, 20)])
+def test_more_rows_than_slots(n, m):
+    """Causal: the first n - m rows see nothing."""
+    Case(2, 2, 1, n, m, 128, 64, "causal", seed=n).check(f"n={n} m={m}")
+
+
+@pytest.mark.parametrize("dk,dv", DIMS)
+@pytest.mark.parametrize("mask,group,n", [("none", 1, 65), ("causal_cache", 4, 100), ("key_padding", 2, 200),
+                                          ("causal", 9, 8)])
+def test_many_rows(dk, dv, mask, group, n):
+    """More than 64 rows per cache head: through bf16 K and V (weights in bf16)."""
+    m = 500
+    lens = [500, 130, 0, 77] if mask in inputs.LENGTH_MASKS else None
+    Case(4, 2, group, n, m, dk, dv, mask, lens, seed=n, slopes=mask == "causal_cache").check(
+        f"{mask} n={n}", many=True)
+
+
+@pytest.mark.parametrize("B,H_kv,group,lens", [
+    (1, 1, 1, [40000]), (70, 3, 2, None), (5, 1, 1, [1, 40000, 0, 2, 9000]), (300, 1, 1, None)])
+def test_uneven_shares(B, H_kv, group, lens):
+    """One pair cut over every CTA; many pairs to a CTA; long ones next to empty ones."""
+    m = 40000 if lens else 1100
+    if lens is None:
+        lens = [(b * 397) % (m + 1) for b in range(B)]
+    Case(B, H_kv, group, 1, m, 64, 64, "key_padding", lens, seed=B).check(f"B={B}")
+
+
+def test_steps_of_very_different_size():
+    """Value and key steps from 2^-20 to 2^10 in one cache: the fp16 operands' scale follows."""
+    g = torch.Generator().manual_seed(3)
+    m = 1500
+    width = torch.exp2(torch.randint(-20, 11, (2, 2, m, 1), generator=g).float())
+    V = (torch.randn(2, 2, m, 128, generator=g) * width).to(torch.bfloat16)
+    K = rows(4, (2, 2, m, 64))
+    for lo, hi in ((0, m), (0, 64), (64, 128)):                   # rising and falling steps, block by block
+        V[:, :, lo:hi] = V[:, :, lo:hi][:, :, torch.argsort(width[0, 0, lo:hi, 0], descending=lo == 64)]
+    c = Case(2, 2, 1, 8, m, 64, 128, "causal", seed=5, K=K, V=V)
+    c.check("steps from 2^-20 to 2^10")
+
+
+def test_a_row_that_sees_only_small_values_next_to_large_ones():
+    """Row 0 sees one slot with values of 2^-20; the slots after it hold values of 2^8."""
+    V = rows(6, (1, 1, 4, 64)).float()
+    V[:, :, 0] *= 2.0 ** -20
+    V[:, :, 1:] *= 2.0 ** 8
+    c = Case(1, 1, 1, 4, 4, 64, 64, "causal", seed=7, V=V.to(torch.bfloat16))
+    c.check("small next to large")
+
+
+@pytest.mark.parametrize("q_scale", [1e-30, 1e-4, 40.0])
+def test_query_magnitudes(q_scale):
+    """The fp16 operand of the query rows is scaled by a power of two of their own."""
+    Case(2, 2, 2, 2, 600, 128, 128, "none", seed=8, q_scale=q_scale).check(f"queries x {q_scale}")
+
+
+def test_rows_with_a_zero_query_take_the_mean():
+    c = Case(1, 2, 1, 2, 777, 64, 64, "none", seed=9, q_scale=0.0)
+    c.check("zero queries")
+    _, L = c.run()
+    assert np.abs(L - np.log(777)).max() <= 1e-5
+
+
+def test_scale():
+    Case(2, 2, 1, 2, 900, 128, 64, "none", seed=10).check("scale", scale=0.31)
+
+
+def test_a_slot_that_cannot_be_held_reaches_only_the_rows_that_see_it():
+    K, V = rows(11, (1, 2, 100, 64)), rows(12, (1, 2, 100, 64))
+    V[0, 0, 99, 5] = float("nan")
+    K[0, 1, 99, 5] = float("inf")
+    c = Case(1, 2, 1, 3, 100, 64, 64, "causal", seed=13, K=K, V=V)
+    O, L = c.run()
+    assert np.isnan(O[0, :, 2]).all() and np.isfinite(O[0, :, :2]).all()
+    args = c.Q[:, :, :2], c.K[:, :, :99]
+    Or, _ = oracle.attn_fwd(*args, c.V[:, :, :99], "causal")
+    bound, _ = oracle.attn_fwd(*args, (c.SU + np.abs(c.V))[:, :, :99], "causal")
+    off = float((np.abs(O[:, :, :2] - Or) - 2.0 ** -8 * np.abs(Or) - 2.0 ** -10.9 * bound).max())
+    assert off <= 0
+
+
+def test_without_lse_and_on_another_stream():
+    c = Case(2, 2, 2, 1, 3000, 128, 128, "causal_cache", [3000, 1234], seed=14)
+    want, _ = c.run()
+    side = torch.cuda.Stream()
+    Q, lens = c.Q.cuda(), i32(c.lens)
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        O, L = attn.decode_q4(Q, c.cache, c.mask, lens, m=c.m, want_lse=False, stream=stream)
+        side.synchronize()
+        assert L is None and np.array_equal(O.double().cpu().numpy(), want)
+
+
+def test_the_same_call_gives_the_same_bits():
+    c = Case(3, 4, 2, 3, 5000, 128, 128, "key_padding", [5000, 4000, 77], seed=15)
+    (O, L), (O2, L2) = c.run(), c.run()
+    assert np.array_equal(O, O2) and np.array_equal(L, L2)
+
+
+def test_decoding_run_through_a_captured_graph():
+    """Tokens written one by one and attended to, lengths advancing on the device: each
+    step equals the oracle on what the cache then holds, and an eager call's bits."""
+    B, H_kv, group, m, steps = 3, 2, 2, 1200, 40
+    K, V = rows(16, (B, H_kv, m, 128)), rows(17, (B, H_kv, m, 128))
+    g = torch.Generator().manual_seed(18)
+    Qs = torch.randn(steps, B, H_kv * group, 1, 128, generator=g).to(torch.bfloat16)
+    first = [0, 63, 1100]
+    cache = torch.full((B, H_kv, -(-m // 64), 34 * 256), 0xFF, dtype=torch.uint8, device="cuda")
+    attn.cache_q4_write(cache, K.cuda(), V.cuda(), None, i32(first), m=m)
+    lens = i32(first)
+    k = torch.empty(B, H_kv, 1, 128, dtype=torch.bfloat16, device="cuda")
+    v, q = torch.empty_like(k), torch.empty(B, H_kv * group, 1, 128, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(attn.decode_q4_workspace_size(B, H_kv * group, H_kv, 1, m, 128, 128), dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        attn.cache_q4_write(cache, k, v, lens, m=m)
+        lens += 1
+        O, L = attn.decode_q4(q, cache, "causal_cache", lens, m=m, workspace=ws)
+    lens.copy_(i32(first))
+    hk, hv = cache_q4.held(K), cache_q4.held(V)
+    for i in range(steps):
+        at = [f + i for f in first]
+        k.copy_(torch.stack([K[b, :, a:a + 1] for b, a in enumerate(at)]))
+        v.copy_(torch.stack([V[b, :, a:a + 1] for b, a in enumerate(at)]))
+        q.copy_(Qs[i])
+        graph.replay()
+        now = [a + 1 for a in at]
+        eager, _ = attn.decode_q4(q, cache, "causal_cache", i32(now), m=m)
+        assert torch.equal(eager, O)
+        if i % 13 == 0:
+            args = (Qs[i], np.repeat(hk, group, 1)), ("causal_cache", now)
+            Or, Lr = oracle.attn_fwd(*args[0], np.repeat(hv, group, 1), *args[1])
+            bound, _ = oracle.attn_fwd(*args[0], np.repeat(cache_q4.coded(V) + np.abs(hv), group, 1), *args[1])
+            err = np.abs(O.double().cpu().numpy() - Or)
+            over = float((err - 2.0 ** -8 * np.abs(Or) - 2.0 ** -10.9 * bound).max())
+            off = float(np.abs(L.cpu().numpy() - Lr).max())
+            assert over <= 0 and off <= 2e-4
+
+
+def test_agrees_with_the_forward_on_the_cache_read_back():
+    c = Case(4, 2, 2, 4, 2500, 64, 64, "key_padding", [2500, 64, 1, 1999], seed=19)
+    O, L = c.run()
+    lens = i32(c.lens)
+    K, V = attn.cache_q4_read(c.cache, 64, 2500, lens, H=4)
+    Of, Lf = attn.attn_fwd(c.Q.cuda(), K, V, "key_padding", lens)
+    torch.cuda.synchronize()
+    # both within their own tolerances of the same reference
+    (_, _, tol, lse_tol), (_, _, tol_f, lse_tol_f) = c.reference(), c.reference(many=True)
+    off = float((np.abs(O - Of.double().cpu().numpy()) - tol - tol_f).max())
+    assert off <= 0
+    off = float(np.abs(L - Lf.double().cpu().numpy()).max())
+    assert off <= lse_tol + lse_tol_f
+
+
+def test_no_slots_and_no_rows():
+    cache = attn.cache_q4_empty(2, 2, 0, 64, 64)
+    Q = torch.randn(2, 4, 3, 64, device="cuda").to(torch.bfloat16)
+    O, L = attn.decode_q4(Q, cache, "none")
+    torch.cuda.synchronize()
+    assert torch.all(O == 0) and torch.all(torch.isneginf(L))
+    O, L = attn.decode_q4(Q[:, :, :0].contiguous(), attn.cache_q4_empty(2, 2, 100, 64, 64), "none", m=100)
+    assert O.numel() == 0
+
+
+def test_forced_timeout_reports_and_recovers():
+    """The bounded wait of the kernel's warps gives up, the status reports it, and a
+    normal call afterwards is right."""
+    c = Case(2, 2, 1, 1, 4096, 128, 128, "none", seed=20)
+    attn.set_watchdog(0, 1)
+    try:
+        attn.decode_q4(c.Q.cuda(), c.cache, "none", m=4096)
+        rc, detail = attn.device_status()
+    finally:
+        attn.set_watchdog(0, 0)
+    assert rc == attn.ATTN_ERR_TIMEOUT and detail & 8
+    c.check("after a timeout")
+
+
+def test_binding_refusals():
+    c = Case(2, 2, 2, 1, 100, 64, 64, "none", seed=21)
+    Q = c.Q.cuda()
+    bad = [lambda: attn.decode_q4(Q, c.cache, "none", m=200), lambda: attn.decode_q4(Q, c.cache, "nothing", m=100),
+           lambda: attn.decode_q4(Q[:1].contiguous(), c.cache, "none", m=100),
+           lambda: attn.decode_q4(Q[:, :3].contiguous(), c.cache, "none", m=100),
+           lambda: attn.decode_q4(Q, c.cache, "key_padding", m=100),
+           lambda: attn.decode_q4(Q, c.cache, "key_padding", i32([1, 2, 3]), m=100),
+           lambda: attn.decode_q4(Q, c.cache, "none", m=100, slopes=torch.ones(2, device="cuda")),
+           lambda: attn.decode_q4(Q.transpose(1, 2), c.cache, "none", m=100),
+           lambda: attn.decode_q4(Q, c.cache, "none", m=100, O=torch.empty(1, device="cuda")),
+           lambda: attn.decode_q4(Q, c.cache.view(torch.int8), "none", m=100),
+           lambda: attn.cache_q4_read(c.cache, 64, 100, first=90, n=11),
+           lambda: attn.cache_q4_read(c.cache, 64, 100, H=3),
+           lambda: attn.cache_q4_read(c.cache, 128, 100),
+           lambda: attn.cache_q4_write(c.cache, Q, Q, m=100),
+           lambda: attn.cache_q4_write(c.cache, Q[:, :2].contiguous(), Q[:, :2].contiguous(), i32([1]), m=100)]
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()

@@ -1,0 +1,178 @@
+"""Pins of the reference of the cache held in 4 bits (no GPU): the definition's
+properties, the format's bytes, and the C ABI's refusals."""
+
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import cache_q4
+from transformer_scaled_dot_03_gb300 import attn, build
+
+
+def rows(seed, shape, spread=1.0):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(shape, generator=g) * spread + torch.randn(shape[-1], generator=g)
+    return x.to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("spread", [1e-3, 1.0, 300.0])
+def test_values_are_bf16_and_within_half_a_step(spread):
+    x = rows(1, (500, 128), spread)
+    u, s, u0, bad = cache_q4.quantise(x)
+    v = cache_q4.held(x)
+    assert not bad.any() and u.min() == 0 and u.max() == 15
+    assert np.array_equal(torch.from_numpy(v).to(torch.bfloat16).double().numpy(), v)
+    assert np.all(np.abs(x.double().numpy() - v) <= np.repeat(s, 64, -1) / 2)
+    # the step: the range's fifteenth, at most an eighth more, four significant bits
+    g = x.double().numpy().reshape(500, 2, 64)
+    t = (np.maximum(g.max(-1), 0) - np.minimum(g.min(-1), 0)) / 15
+    assert np.all(s >= t * (1 - 2.0 ** -23)) and np.all(s <= t * 1.125 * (1 + 2.0 ** -23))
+    frac, _ = np.frexp(s)
+    assert np.array_equal(frac * 16, np.rint(frac * 16))
+
+
+def test_zero_is_held_exactly_and_ties_go_to_even():
+    x = torch.zeros(64, dtype=torch.bfloat16)
+    assert np.all(cache_q4.held(x) == 0)
+    # s = 1 (range 0..15): 0.5 -> 0, 1.5 -> 2, 2.5 -> 2
+    x[:5] = torch.tensor([15.0, 0.5, 1.5, 2.5, 7.25])
+    u, s, u0, _ = cache_q4.quantise(x)
+    assert s[0] == 1 and u0[0] == 0 and list(u[:5]) == [15, 0, 2, 2, 7]
+    # one sign only: the range still reaches 0
+    x = torch.full((64,), -3.0, dtype=torch.bfloat16)
+    u, s, u0, _ = cache_q4.quantise(x)
+    assert u0[0] == 15 or cache_q4.held(x).max() < 0
+    assert np.all(np.abs(cache_q4.held(x) + 3.0) <= s[0] / 2)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf"), 2.0 ** 127])
+def test_a_group_that_cannot_be_held_is_nan(bad):
+    x = rows(2, (3, 128))
+    x[1, 70] = bad
+    v = cache_q4.held(x)
+    assert np.isnan(v[1, 64:]).all() and np.isfinite(v[1, :64]).all() and np.isfinite(v[[0, 2]]).all()
+
+
+def test_subnormal_and_largest_magnitudes():
+    for scale in (2.0 ** -130, 2.0 ** -120, 2.0 ** 120):
+        x = (rows(3, (50, 64)).float().clamp(-4, 4).double() * scale).to(torch.bfloat16)
+        u, s, u0, bad = cache_q4.quantise(x)
+        v = cache_q4.held(x)
+        assert not bad.any() and np.isfinite(v).all()
+        assert np.all(np.abs(x.double().numpy() - v) <= np.repeat(s, 64, -1) / 2)
+        assert np.array_equal(torch.from_numpy(v).to(torch.bfloat16).double().numpy(), v)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("is_k", [True, False])
+def test_every_code_has_a_place_of_its_own(d, is_k):
+    seen = {cache_q4.code_byte(k, c, d, is_k) for k in range(64) for c in range(d)}
+    assert len(seen) == 64 * d
+    assert {b for b, _ in seen} == set(range(32 * d))
+    # a slot's row is d / 2 contiguous bytes
+    for k in range(64):
+        at = {cache_q4.code_byte(k, c, d, is_k)[0] for c in range(d)}
+        assert max(at) - min(at) == d // 2 - 1
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128), (64, 128), (128, 64)])
+def test_write_and_read(dk, dv):
+    rng = np.random.default_rng(4)
+    cache = rng.integers(0, 256, (3, 2, 3, 34 * (dk + dv)), dtype=np.uint8)
+    K, V = rows(5, (3, 2, 20, dk)), rows(6, (3, 2, 20, dv))
+    starts, counts = [0, 55, 140], [20, 20, 7]
+    out = cache_q4.write(cache, K, V, starts, counts, m=150)
+    hk, hv = cache_q4.held(K), cache_q4.held(V)
+    rk, rv = cache_q4.read(out, dk, 150)
+    ok, ov = cache_q4.read(cache, dk, 150)
+    for b in range(3):
+        a, c = starts[b], min(counts[b], 150 - starts[b])
+        assert np.array_equal(rk[b, :, a:a + c], hk[b, :, :c]) and np.array_equal(rv[b, :, a:a + c], hv[b, :, :c])
+        rest = np.r_[0:a, a + c:150]
+        assert np.array_equal(rk[b, :, rest], ok[b, :, rest], equal_nan=True)
+        assert np.array_equal(rv[b, :, rest], ov[b, :, rest], equal_nan=True)
+    assert np.all(cache_q4.read(out, dk, 150, [5, 0, 150])[0][1] == 0)
+
+
+# ---------------------------------------------------------------- the C ABI's refusals
+
+P, P2 = ctypes.c_void_p(0x10000), ctypes.c_void_p(0x20000)     # never dereferenced: rejected first
+ODD = ctypes.c_void_p(0x10008)
+INVALID, UNSUPPORTED, MISALIGNED = attn.ATTN_ERR_INVALID_ARG, attn.ATTN_ERR_UNSUPPORTED, attn.ATTN_ERR_MISALIGNED
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return attn.load()
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(B=-1), INVALID), (dict(n=-1), INVALID), (dict(m=-1), INVALID), (dict(H=-2), INVALID),
+    (dict(dk=96), UNSUPPORTED), (dict(dv=32), UNSUPPORTED), (dict(m=(1 << 30) + 1), UNSUPPORTED),
+    (dict(n=1 << 29, H=8), UNSUPPORTED),
+    (dict(K=None), INVALID), (dict(V=None), INVALID), (dict(cache=None), INVALID),
+    (dict(K=ODD), MISALIGNED), (dict(cache=ODD), MISALIGNED), (dict(starts=ctypes.c_void_p(0x30002)), MISALIGNED),
+    (dict(counts=ctypes.c_void_p(0x30001)), MISALIGNED),
+    (dict(n=0), attn.ATTN_OK), (dict(B=0, K=None), attn.ATTN_OK), (dict(m=0), attn.ATTN_OK),
+])
+def test_write_refusals(lib, kw, code):
+    a = dict(K=P, V=P, B=1, H=2, n=3, m=100, dk=64, dv=64, starts=None, counts=None, cache=P2)
+    a.update(kw)
+    assert lib.attn_cache_q4_write(a["K"], a["V"], a["B"], a["H"], a["n"], a["m"], a["dk"], a["dv"], a["starts"],
+                                   a["counts"], a["cache"], None) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(H=3), INVALID), (dict(Hk=0), INVALID), (dict(first=-1), INVALID), (dict(first=98, n=3), INVALID),
+    (dict(n=101), INVALID), (dict(first=(1 << 31) - 1, n=(1 << 31) - 1), INVALID), (dict(dk=32), UNSUPPORTED),
+    (dict(K=None), INVALID), (dict(cache=None), INVALID), (dict(V=ODD), MISALIGNED), (dict(cache=ODD), MISALIGNED),
+    (dict(lens=ctypes.c_void_p(0x30002)), MISALIGNED), (dict(n=0), attn.ATTN_OK), (dict(B=0), attn.ATTN_OK),
+])
+def test_read_refusals(lib, kw, code):
+    a = dict(cache=P, B=1, H=4, Hk=2, m=100, first=0, n=100, dk=64, dv=64, lens=None, K=P2, V=P2)
+    a.update(kw)
+    assert lib.attn_cache_q4_read(a["cache"], a["B"], a["H"], a["Hk"], a["m"], a["first"], a["n"], a["dk"], a["dv"],
+                                  a["lens"], a["K"], a["V"], None) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(H=3), INVALID), (dict(Hk=0), INVALID), (dict(n=-1), INVALID), (dict(mask=5), INVALID),
+    (dict(mask=4), INVALID), (dict(mask=2), INVALID), (dict(dk=256), UNSUPPORTED), (dict(dv=96), UNSUPPORTED),
+    (dict(Q=None), INVALID), (dict(O=None), INVALID), (dict(ws=None), INVALID), (dict(ws_bytes=100), INVALID),
+    (dict(ws=ctypes.c_void_p(0x10040)), MISALIGNED), (dict(Q=ODD), MISALIGNED), (dict(cache=ODD), MISALIGNED),
+    (dict(O=ODD), MISALIGNED), (dict(LSE=ctypes.c_void_p(0x30002)), MISALIGNED),
+    (dict(slopes=ctypes.c_void_p(0x30002)), MISALIGNED), (dict(n=1000, ws_bytes=1 << 20), INVALID),
+    (dict(n=0), attn.ATTN_OK), (dict(B=0), attn.ATTN_OK),
+])
+def test_decode_refusals(lib, kw, code):
+    a = dict(Q=P, cache=P, B=1, H=4, Hk=2, n=1, m=8192, dk=64, dv=64, mask=0, lens=None, slopes=None, O=P2, LSE=None,
+             ws=P, ws_bytes=1 << 30)
+    a.update(kw)
+    assert lib.attn_decode_q4(a["Q"], a["cache"], a["B"], a["H"], a["Hk"], a["n"], a["m"], a["dk"], a["dv"], a["mask"],
+                              a["lens"], a["slopes"], -1.0, a["O"], a["LSE"], a["ws"], a["ws_bytes"], None) == code
+
+
+def test_sizes(lib):
+    assert lib.attn_cache_q4_size(2, 3, 64, 64, 64) == 6 * 34 * 128
+    assert lib.attn_cache_q4_size(2, 3, 65, 128, 64) == 12 * 34 * 192
+    assert lib.attn_cache_q4_size(0, 3, 65, 128, 64) == 0
+    assert lib.attn_cache_q4_size(1, 1, 65, 96, 64) == 0
+    # 17/64 of the bf16 cache
+    assert lib.attn_cache_q4_size(64, 16, 8192, 128, 128) * 64 == 64 * 16 * 8192 * 512 * 17
+    assert attn.decode_q4_workspace_size(8, 8, 8, 1, 64, 64, 64) == 0
+    # many rows: the cache as bf16, for every query head
+    assert attn.decode_q4_workspace_size(2, 8, 4, 100, 4096, 128, 64) == 2 * 8 * 4096 * 192 * 2
+    # few rows: bounded however large the batch and the cache are
+    assert attn.decode_q4_workspace_size(512, 32, 8, 8, 131072, 128, 128) < 64 << 20
+
+
+def test_binding_refuses(lib):
+    x = torch.zeros(1, 2, 4, 64, dtype=torch.bfloat16)
+    c = torch.zeros(1, 2, 1, 34 * 128, dtype=torch.uint8)
+    for call in (lambda: attn.cache_q4_write(c, x, x), lambda: attn.cache_q4_read(c, 64),
+                 lambda: attn.decode_q4(x, c)):
+        with pytest.raises(ValueError):
+            call()

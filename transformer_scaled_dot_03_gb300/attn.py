@@ -9,6 +9,7 @@ if the library is missing or no GPU is present, the call raises.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -35,7 +36,10 @@ MASK_CODES = {_inputs.MASK_NONE: 0, _inputs.MASK_CAUSAL: 1, _inputs.MASK_KEY_PAD
 EXPORTS = ("attn_fwd", "attn_fwd_alibi", "attn_decode_alibi", "attn_bwd_alibi", "attn_get_device_status",
            "attn_last_status_detail", "attn_set_watchdog", "attn_status_string", "attn_last_error",
            "attn_fwd_noalloc", "attn_bwd", "attn_bwd_workspace_size", "attn_decode",
-           "attn_decode_workspace_size", "attn_proj_heads", "attn_merge_proj")
+           "attn_decode_workspace_size", "attn_proj_heads", "attn_merge_proj", "attn_cache_q4_size",
+           "attn_cache_q4_write", "attn_cache_q4_read", "attn_decode_q4", "attn_decode_q4_workspace_size")
+
+CACHE_Q4_BLOCK = 64               # slots per block of a cache held in 4 bits
 
 _lock = threading.Lock()
 _lib = None
@@ -92,6 +96,17 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.attn_proj_heads.restype = i32
         lib.attn_merge_proj.argtypes = [vp, vp, vp, i32, i32, i32, i32, i32, vp, vp]
         lib.attn_merge_proj.restype = i32
+        sz = ctypes.c_size_t
+        lib.attn_cache_q4_size.argtypes = [i32] * 5
+        lib.attn_cache_q4_size.restype = sz
+        lib.attn_cache_q4_write.argtypes = [vp, vp, i32, i32, i32, i32, i32, i32, vp, vp, vp, vp]
+        lib.attn_cache_q4_write.restype = i32
+        lib.attn_cache_q4_read.argtypes = [vp, i32, i32, i32, i32, i32, i32, i32, i32, vp, vp, vp, vp]
+        lib.attn_cache_q4_read.restype = i32
+        lib.attn_decode_q4_workspace_size.argtypes = [i32] * 7
+        lib.attn_decode_q4_workspace_size.restype = sz
+        lib.attn_decode_q4.argtypes = [vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, vp, vp, f32, vp, vp, vp, sz, vp]
+        lib.attn_decode_q4.restype = i32
         lib.attn_last_error.argtypes = []
         lib.attn_last_error.restype = ctypes.c_char_p
         _lib = lib
@@ -379,6 +394,156 @@ def merge_proj(O: torch.Tensor, W_o: torch.Tensor, bias: torch.Tensor | None = N
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_merge_proj", last_error() if rc == ATTN_ERR_CUDA else "")
     return Y
+
+
+@contextlib.contextmanager
+def _on(device, stream):
+    """Run on ``device`` and ``stream`` (a torch stream, a cudaStream_t as an int, or None
+    for the device's current stream); yields the stream's handle. What is allocated
+    inside belongs to that stream, so that its memory is not handed on while a kernel
+    there still uses it."""
+    with torch.cuda.device(device):
+        if stream is None:
+            yield int(torch.cuda.current_stream().cuda_stream)
+            return
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        with torch.cuda.stream(stream):
+            yield int(stream.cuda_stream)
+
+
+def _cuda_arg(name, t, dtype, shape, device):
+    """Check an argument (``shape`` as a tuple) that must lie contiguous on ``device``."""
+    if t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {device}")
+
+
+def cache_q4_empty(B: int, H_kv: int, m: int, d_k: int, d_v: int, device="cuda") -> torch.Tensor:
+    """An uninitialised key/value cache of ``m`` slots held in 4 bits: a uint8 tensor
+    [B, H_kv, ceil(m / 64), 34 (d_k + d_v)] (the layout is in ``include/attn.h``)."""
+    return torch.empty((B, H_kv, -(-m // CACHE_Q4_BLOCK), 34 * (d_k + d_v)), dtype=torch.uint8, device=device)
+
+
+def _cache_q4_dims(cache, d_k, m):
+    """Check the cache tensor; (B, H_kv, m, d_v) with ``m`` slots (None: all of its blocks')."""
+    if cache.dtype != torch.uint8 or not cache.is_cuda or cache.dim() != 4 or not cache.is_contiguous() \
+            or cache.shape[3] % 34 != 0:
+        raise ValueError("cache must be a contiguous uint8 CUDA tensor [B, H_kv, blocks, 34 (d_k + d_v)]")
+    B, H_kv, blocks, width = cache.shape
+    m = blocks * CACHE_Q4_BLOCK if m is None else int(m)
+    if m < 0 or -(-m // CACHE_Q4_BLOCK) != blocks:
+        raise ValueError(f"a cache of {m} slots has {-(-m // CACHE_Q4_BLOCK)} blocks, not {blocks}")
+    if not 0 < d_k < width // 34:
+        raise ValueError(f"the cache's rows are {width // 34} channels wide in all: no room for d_k = {d_k} and a d_v")
+    return B, H_kv, m, width // 34 - d_k
+
+
+def cache_q4_write(cache: torch.Tensor, K: torch.Tensor, V: torch.Tensor, starts: torch.Tensor | None = None,
+                   counts: torch.Tensor | None = None, m: int | None = None, stream=None) -> torch.Tensor:
+    """Quantise new rows K [B,H_kv,n,d_k], V [B,H_kv,n,d_v] (contiguous bf16) into the cache:
+    row i of entry b goes to slot ``starts[b] + i`` (int32 CUDA [B], None: 0) for
+    i < ``counts[b]`` (None: n); rows outside the ``m`` slots (None: all of the cache's blocks) are skipped and
+    every other slot keeps its bytes. Returns ``cache``. Asynchronous on ``stream``."""
+    _bf16_cuda("K", K, 4)
+    _bf16_cuda("V", V, 4)
+    B, H_kv, n, d_k = K.shape
+    d_v = V.shape[3]
+    cB, cH, m, c_dv = _cache_q4_dims(cache, d_k, m)
+    if tuple(V.shape[:3]) != (B, H_kv, n) or (cB, cH, c_dv) != (B, H_kv, d_v):
+        raise ValueError("inconsistent K/V/cache shapes")
+    dev = cache.device
+    if K.device != dev or V.device != dev:
+        raise ValueError("K, V and the cache must be on one device")
+    for name, t in (("starts", starts), ("counts", counts)):
+        if t is not None:
+            _cuda_arg(name, t, torch.int32, (B,), dev)
+    with _on(dev, stream) as handle:
+        rc = load().attn_cache_q4_write(_ptr(K), _ptr(V), B, H_kv, n, m, d_k, d_v, _ptr(starts), _ptr(counts),
+                                        _ptr(cache), ctypes.c_void_p(handle))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_cache_q4_write", last_error() if rc == ATTN_ERR_CUDA else "")
+    return cache
+
+
+def cache_q4_read(cache: torch.Tensor, d_k: int, m: int | None = None, key_lengths: torch.Tensor | None = None,
+                  H: int | None = None, first: int = 0, n: int | None = None, K: torch.Tensor | None = None,
+                  V: torch.Tensor | None = None, stream=None):
+    """The cache's slots ``first`` .. ``first + n - 1`` (default: all ``m``) as bf16
+    (K [B,H,n,d_k], V [B,H,n,d_v]), exactly the values held; each cache head is copied to
+    its H / H_kv query heads (``H`` defaults to H_kv). Slots at or past ``key_lengths[b]``
+    (int32 CUDA [B]) give 0. Asynchronous on ``stream``."""
+    B, H_kv, m, d_v = _cache_q4_dims(cache, d_k, m)
+    H = H_kv if H is None else int(H)
+    n = m - first if n is None else int(n)
+    dev = cache.device
+    if first < 0 or n < 0 or first + n > m or H < 0 or (H % H_kv if H_kv else H):
+        raise ValueError("slots outside the cache, or H not a multiple of its heads")
+    if key_lengths is not None:
+        _cuda_arg("key_lengths", key_lengths, torch.int32, (B,), dev)
+    for name, t, d in (("K", K, d_k), ("V", V, d_v)):
+        if t is not None:
+            _cuda_arg(name, t, torch.bfloat16, (B, H, n, d), dev)
+    with _on(dev, stream) as handle:
+        K = torch.empty((B, H, n, d_k), dtype=torch.bfloat16, device=dev) if K is None else K
+        V = torch.empty((B, H, n, d_v), dtype=torch.bfloat16, device=dev) if V is None else V
+        rc = load().attn_cache_q4_read(_ptr(cache), B, H, H_kv, m, int(first), n, d_k, d_v, _ptr(key_lengths), _ptr(K),
+                                       _ptr(V), ctypes.c_void_p(handle))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_cache_q4_read", last_error() if rc == ATTN_ERR_CUDA else "")
+    return K, V
+
+
+def decode_q4_workspace_size(B, H, H_kv, n, m, d_k, d_v) -> int:
+    return int(load().attn_decode_q4_workspace_size(int(B), int(H), int(H_kv), int(n), int(m), int(d_k), int(d_v)))
+
+
+def decode_q4(Q: torch.Tensor, cache: torch.Tensor, mask: str = "none", key_lengths: torch.Tensor | None = None,
+              scale: float | None = None, m: int | None = None, slopes: torch.Tensor | None = None,
+              O: torch.Tensor | None = None, LSE: torch.Tensor | None = None, want_lse: bool = True,
+              workspace: torch.Tensor | None = None, stream=None):
+    """``attn_decode`` over a cache held in 4 bits: Q [B,H,n,d_k] (contiguous bf16), H a multiple of the
+    cache's heads, ``m`` its slots (None: all of its blocks'); masks, lengths, scale
+    and results as in ``attn_fwd``, ``slopes`` (fp32 CUDA [H]) the distance bias of
+    ``attn_fwd_alibi``. ``workspace`` (uint8 CUDA tensor of at least
+    ``decode_q4_workspace_size`` bytes, for one call at a time) is allocated here when
+    omitted and needed. Returns (O, LSE or None). Asynchronous on ``stream``."""
+    if mask not in MASK_CODES:
+        raise ValueError(f"unknown mask {mask!r}")
+    _bf16_cuda("Q", Q, 4)
+    B, H, n, d_k = Q.shape
+    cB, H_kv, m, d_v = _cache_q4_dims(cache, d_k, m)
+    dev = cache.device
+    if cB != B or Q.device != dev or (H % H_kv if H_kv else H):
+        raise ValueError("Q and the cache must have the same batch and device, and H be a multiple of the cache's heads")
+    uses_lengths = mask in _inputs.LENGTH_MASKS
+    if uses_lengths:
+        if key_lengths is None:
+            raise ValueError(f"{mask} needs key_lengths: contiguous int32 CUDA [B]")
+        _cuda_arg("key_lengths", key_lengths, torch.int32, (B,), dev)
+    if slopes is not None:
+        _cuda_arg("slopes", slopes, torch.float32, (H,), dev)
+    if O is not None:
+        _cuda_arg("O", O, torch.bfloat16, (B, H, n, d_v), dev)
+    if LSE is not None:
+        _cuda_arg("LSE", LSE, torch.float32, (B, H, n), dev)
+    ws_bytes = decode_q4_workspace_size(B, H, H_kv, n, m, d_k, d_v)
+    if workspace is not None and (workspace.dtype != torch.uint8 or workspace.device != dev
+                                  or workspace.numel() < ws_bytes or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {ws_bytes} bytes on {dev}")
+    with _on(dev, stream) as handle:
+        O = torch.empty((B, H, n, d_v), dtype=torch.bfloat16, device=dev) if O is None else O
+        if LSE is None and want_lse:
+            LSE = torch.empty((B, H, n), dtype=torch.float32, device=dev)
+        if workspace is None and ws_bytes > 0:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        rc = load().attn_decode_q4(_ptr(Q), _ptr(cache), B, H, H_kv, n, m, d_k, d_v, MASK_CODES[mask],
+                                   _ptr(key_lengths) if uses_lengths else None, _ptr(slopes),
+                                   ctypes.c_float(-1.0 if scale is None else float(scale)), _ptr(O), _ptr(LSE),
+                                   _ptr(workspace), ctypes.c_size_t(0 if workspace is None else workspace.numel()),
+                                   ctypes.c_void_p(handle))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_decode_q4", last_error() if rc == ATTN_ERR_CUDA else "")
+    return O, LSE
 
 
 def device_status(stream=None) -> tuple[int, int]:

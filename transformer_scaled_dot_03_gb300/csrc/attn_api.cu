@@ -15,6 +15,7 @@
 #include <cudaTypedefs.h>
 
 #include "../../include/attn.h"
+#include "attn_cache_q4.cuh"
 #include "attn_internal.h"
 #include "sm103a.cuh"
 
@@ -963,4 +964,222 @@ extern "C" int attn_merge_proj(const void* O, const void* W_o, const void* bias,
     p.a_box_rows = static_cast<int>(a_rows);
     p.bias = static_cast<const uint16_t*>(bias);
     return run_proj(true, false, maps, p, static_cast<cudaStream_t>(stream));
+}
+
+// ---------------------------------------------------------------------------
+// A key/value cache held in 4 bits: writing, reading back, attention over it.
+namespace {
+
+constexpr int kQ4MaxRows = 64;            // rows per cache head up to which the few-row kernel runs
+constexpr int64_t kQ4MaxCtas = 1024;      // bound on its split grid, used to size the workspace
+constexpr int kQ4SplitBlocks = 16;        // more blocks than this per (b, cache head) are split over CTAs
+
+// Sizes that every entry point on the cache shares.
+int q4_validate(int B, int H_kv, int m, int d_k, int d_v)
+{
+    if (B < 0 || H_kv < 0 || m < 0) return ATTN_ERR_INVALID_ARG;
+    if (!head_dim_ok(d_k) || !head_dim_ok(d_v)) return ATTN_ERR_UNSUPPORTED;
+    if (m > kMaxSeq || static_cast<int64_t>(B) * H_kv > INT32_MAX) return ATTN_ERR_UNSUPPORTED;
+    return ATTN_OK;
+}
+
+int q4_blocks(int m) { return static_cast<int>((static_cast<int64_t>(m) + attn::q4::BLOCK - 1) / attn::q4::BLOCK); }
+
+// Scratch of attn_decode_q4: the parts of split pairs, or for many rows K and V as bf16.
+struct Q4Plan {
+    bool few, split;
+    int rows, row_tiles;              // rows per cache head, tiles of them
+    int64_t pairs, ctas;              // (b, cache head, row tile) triples; largest split grid
+    int part_rows;
+    size_t ml_off, flags_off;         // split
+    size_t v_off;                     // many rows
+    size_t total;
+};
+
+Q4Plan q4_plan(int64_t B, int64_t H, int64_t H_kv, int64_t n, int m, int d_k, int d_v)
+{
+    Q4Plan w = {};
+    const int64_t R = H / H_kv * n;
+    w.few = R <= kQ4MaxRows;
+    if (!w.few) {
+        w.v_off = round_up(static_cast<size_t>(B * H) * m * d_k * 2, kWsAlign);
+        w.total = w.v_off + round_up(static_cast<size_t>(B * H) * m * d_v * 2, kWsAlign);
+        return w;
+    }
+    const int tile = attn::decode_q4_tile_rows(static_cast<int>(R));
+    w.rows = static_cast<int>(R);
+    w.row_tiles = (w.rows + tile - 1) / tile;
+    w.pairs = B * H_kv * w.row_tiles;
+    const int64_t blocks = q4_blocks(m);
+    w.split = blocks > kQ4SplitBlocks;
+    if (!w.split) return w;
+    w.ctas = std::max<int64_t>(1, std::min(kQ4MaxCtas, w.pairs * blocks / 4));
+    w.part_rows = std::min(w.rows, tile);
+    const size_t parts = static_cast<size_t>(2 * w.ctas) * w.part_rows;
+    w.ml_off = round_up(parts * d_v * 4, kWsAlign);
+    w.flags_off = w.ml_off + round_up(parts * 2 * 4, kWsAlign);
+    w.total = w.flags_off + round_up(static_cast<size_t>(w.ctas) * 8, kWsAlign);
+    return w;
+}
+
+int q4_read(const void* cache, int B, int H, int H_kv, int m, int first, int n, int d_k, int d_v,
+            const int32_t* key_lengths, void* K, void* V, cudaStream_t st)
+{
+    attn::CacheQ4ReadParams p;
+    p.cache = static_cast<const uint8_t*>(cache);
+    p.B = B;
+    p.H = H;
+    p.H_kv = H_kv;
+    p.group = H / H_kv;
+    p.m = m;
+    p.first = first;
+    p.n = n;
+    p.tiles = q4_blocks(n);
+    p.d_k = d_k;
+    p.d_v = d_v;
+    p.blocks = q4_blocks(m);
+    p.key_lengths = key_lengths;
+    p.K = static_cast<uint16_t*>(K);
+    p.V = static_cast<uint16_t*>(V);
+    if (static_cast<int64_t>(B) * H_kv * p.tiles > INT32_MAX) return ATTN_ERR_UNSUPPORTED;
+    const cudaError_t e = attn::launch_cache_q4_read(p, st);
+    return e == cudaSuccess ? ATTN_OK : fail_cuda("cache read kernel launch", e);
+}
+
+}  // namespace
+
+extern "C" size_t attn_cache_q4_size(int B, int H_kv, int m, int d_k, int d_v)
+{
+    if (B <= 0 || H_kv <= 0 || m <= 0 || !head_dim_ok(d_k) || !head_dim_ok(d_v)) return 0;
+    return static_cast<size_t>(B) * H_kv * q4_blocks(m) * attn::q4::block_bytes(d_k, d_v);
+}
+
+extern "C" int attn_cache_q4_write(const void* K, const void* V, int B, int H_kv, int n, int m, int d_k, int d_v,
+                                   const int32_t* starts, const int32_t* counts, void* cache, void* stream)
+{
+    int rc = q4_validate(B, H_kv, m, d_k, d_v);
+    if (rc != ATTN_OK) return rc;
+    if (n < 0) return ATTN_ERR_INVALID_ARG;
+    if (n > kMaxSeq) return ATTN_ERR_UNSUPPORTED;
+    if (B == 0 || H_kv == 0 || n == 0 || m == 0) return ATTN_OK;
+    const int64_t rows = static_cast<int64_t>(B) * H_kv * n;
+    const int64_t groups = rows <= INT32_MAX ? rows * ((d_k + d_v) / attn::q4::GROUP) : INT64_MAX;
+    if (groups > INT32_MAX) return ATTN_ERR_UNSUPPORTED;
+    if (K == nullptr || V == nullptr || cache == nullptr) return ATTN_ERR_INVALID_ARG;
+    if (!aligned(K, 16) || !aligned(V, 16) || !aligned(cache, 16) || (starts != nullptr && !aligned(starts, 4)) ||
+        (counts != nullptr && !aligned(counts, 4)))
+        return ATTN_ERR_MISALIGNED;
+    attn::CacheQ4WriteParams p;
+    p.K = static_cast<const uint16_t*>(K);
+    p.V = static_cast<const uint16_t*>(V);
+    p.H = H_kv;
+    p.n = n;
+    p.m = m;
+    p.d_k = d_k;
+    p.d_v = d_v;
+    p.blocks = q4_blocks(m);
+    p.k_groups = static_cast<uint32_t>(rows * (d_k / attn::q4::GROUP));
+    p.groups = static_cast<uint32_t>(groups);
+    p.starts = starts;
+    p.counts = counts;
+    p.cache = static_cast<uint8_t*>(cache);
+    const cudaError_t e = attn::launch_cache_q4_write(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ATTN_OK : fail_cuda("cache write kernel launch", e);
+}
+
+extern "C" int attn_cache_q4_read(const void* cache, int B, int H, int H_kv, int m, int first, int n, int d_k, int d_v,
+                                  const int32_t* key_lengths, void* K, void* V, void* stream)
+{
+    int rc = q4_validate(B, H_kv, m, d_k, d_v);
+    if (rc != ATTN_OK) return rc;
+    if (H < 0 || n < 0 || first < 0 || static_cast<int64_t>(first) + n > m) return ATTN_ERR_INVALID_ARG;
+    if (H_kv > 0 ? H % H_kv != 0 : H != 0) return ATTN_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(B) * H > INT32_MAX) return ATTN_ERR_UNSUPPORTED;
+    if (B == 0 || H == 0 || n == 0) return ATTN_OK;
+    if (cache == nullptr || K == nullptr || V == nullptr) return ATTN_ERR_INVALID_ARG;
+    if (!aligned(cache, 16) || !aligned(K, 16) || !aligned(V, 16) || (key_lengths != nullptr && !aligned(key_lengths, 4)))
+        return ATTN_ERR_MISALIGNED;
+    return q4_read(cache, B, H, H_kv, m, first, n, d_k, d_v, key_lengths, K, V, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" size_t attn_decode_q4_workspace_size(int B, int H, int H_kv, int n, int m, int d_k, int d_v)
+{
+    if (B <= 0 || H <= 0 || H_kv <= 0 || H % H_kv != 0 || n <= 0 || m <= 0 || !head_dim_ok(d_k) || !head_dim_ok(d_v))
+        return 0;
+    return q4_plan(B, H, H_kv, n, m, d_k, d_v).total;
+}
+
+extern "C" int attn_decode_q4(const void* Q, const void* cache, int B, int H, int H_kv, int n, int m, int d_k, int d_v,
+                              int mask_kind, const int32_t* key_lengths, const float* slopes, float scale, void* O,
+                              float* LSE, void* workspace, size_t workspace_bytes, void* stream)
+{
+    int rc = q4_validate(B, H_kv, m, d_k, d_v);
+    if (rc != ATTN_OK) return rc;
+    if (H < 0 || n < 0) return ATTN_ERR_INVALID_ARG;
+    if (H_kv > 0 ? H % H_kv != 0 : H != 0) return ATTN_ERR_INVALID_ARG;
+    if (mask_kind < ATTN_MASK_NONE || mask_kind > ATTN_MASK_CAUSAL_CACHE) return ATTN_ERR_INVALID_ARG;
+    if (attn::mask_has_lengths(mask_kind) && key_lengths == nullptr) return ATTN_ERR_INVALID_ARG;
+    const int64_t bh = static_cast<int64_t>(B) * H;
+    const int64_t num_qblocks = (static_cast<int64_t>(n) + 127) / 128;
+    if (n > kMaxSeq || bh > INT32_MAX || bh * num_qblocks > INT32_MAX) return ATTN_ERR_UNSUPPORTED;
+    if (B == 0 || H == 0 || n == 0) return ATTN_OK;
+    if (O == nullptr || (m > 0 && (Q == nullptr || cache == nullptr))) return ATTN_ERR_INVALID_ARG;
+    if (!aligned(O, 16) || !aligned(Q, 16) || !aligned(cache, 16) || (LSE != nullptr && !aligned(LSE, 4)) ||
+        (key_lengths != nullptr && !aligned(key_lengths, 4)) || (slopes != nullptr && !aligned(slopes, 4)))
+        return ATTN_ERR_MISALIGNED;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (m == 0) return fill_no_keys(bh, n, d_v, O, LSE, st);
+    const Q4Plan w = q4_plan(B, H, H_kv, n, m, d_k, d_v);
+    if (w.total > 0 && (workspace == nullptr || workspace_bytes < w.total)) return ATTN_ERR_INVALID_ARG;
+    if (w.total > 0 && !aligned(workspace, kWsAlign)) return ATTN_ERR_MISALIGNED;
+    if (w.few && w.pairs > INT32_MAX) return ATTN_ERR_UNSUPPORTED;
+    uint32_t* status = nullptr;
+    if ((rc = status_word(&status)) != ATTN_OK) return rc;
+    uint8_t* wsb = static_cast<uint8_t*>(workspace);
+    const int32_t* lens = attn::mask_has_lengths(mask_kind) ? key_lengths : nullptr;
+
+    if (!w.few) {
+        // many rows: the cache as bf16, then the tensor-core forward
+        rc = q4_read(cache, B, H, H_kv, m, 0, m, d_k, d_v, lens, wsb, wsb + w.v_off, st);
+        if (rc != ATTN_OK) return rc;
+        return launch_attention(Q, wsb, wsb + w.v_off, B, H, n, m, d_k, d_v, mask_kind, lens, scale, O, LSE, status, st,
+                                slopes);
+    }
+
+    const double sc = (scale > 0.f && std::isfinite(scale)) ? static_cast<double>(scale)
+                                                             : 1.0 / std::sqrt(static_cast<double>(d_k));
+    attn::DecodeQ4Params p;
+    p.Q = static_cast<const uint16_t*>(Q);
+    p.cache = static_cast<const uint8_t*>(cache);
+    p.B = B;
+    p.H_kv = H_kv;
+    p.n = n;
+    p.m = m;
+    p.R = w.rows;
+    p.row_tiles = w.row_tiles;
+    p.blocks = q4_blocks(m);
+    p.mask = mask_kind;
+    p.key_lengths = lens;
+    p.slopes = slopes;
+    p.scale_log2 = static_cast<float>(sc * 1.4426950408889634074);
+    p.split = w.split ? 1 : 0;
+    p.ctas = static_cast<int>(w.pairs);
+    if (w.split) {
+        int num_sms = 0;
+        if ((rc = sm_count(&num_sms)) != ATTN_OK) return rc;
+        const int64_t slots = static_cast<int64_t>(num_sms) *
+                              attn::decode_q4_ctas_per_sm(d_k, d_v, attn::decode_q4_tile_rows(w.rows));
+        p.ctas = static_cast<int>(std::min(slots, w.ctas));
+    }
+    p.O = static_cast<uint16_t*>(O);
+    p.LSE = LSE;
+    p.part_o = reinterpret_cast<float*>(wsb);
+    p.part_ml = reinterpret_cast<float*>(wsb + w.ml_off);
+    p.part_flags = reinterpret_cast<int2*>(wsb + w.flags_off);
+    p.part_rows = w.part_rows;
+    p.status = status;
+    p.watchdog_ns = g_watchdog_ns;
+    p.debug_flags = g_debug_flags;
+    const cudaError_t e = attn::launch_decode_q4(d_k, d_v, p, st);
+    return e == cudaSuccess ? ATTN_OK : fail_cuda("4-bit decode kernel launch", e);
 }

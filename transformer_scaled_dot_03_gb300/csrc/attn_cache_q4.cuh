@@ -1,0 +1,59 @@
+// attn_cache_q4.cuh -- the format of a key/value cache held in 4 bits, shared by
+// the kernels that write it, read it back and attend over it.
+//
+// Quantisation. A group is 64 channels of one token and head. With
+// lo = min(0, min x) and hi = max(0, max x):
+//
+//     s  = (hi - lo) / 15 rounded up to four significant bits,
+//     u0 = rint(-lo / s) in 0..15,   u = clamp(rint(x / s) + u0, 0, 15),
+//     value = s (u - u0),            |x - value| <= s / 2.
+//
+// |u - u0| has four bits and s has four, so every value is a bf16 number: the
+// cache read back as bf16 and the cache attended over in place are the same
+// numbers. s as bf16 has its four low mantissa bits free, which hold u0: one
+// 16-bit word a group, 4.25 bits a value. A group with a NaN, an infinity or a
+// magnitude of 2^127 or more gets the word 0x7FC0 (s = NaN).
+//
+// Layout. [B][H_kv][ceil(m / 64)] blocks of 64 slots, 34 (d_k + d_v) bytes each and
+// contiguous, so that one bulk copy brings a block: K codes (32 d_k bytes), K words
+// (2 d_k), V codes (32 d_v), V words (2 d_v). Words lie as [slot][group]. The codes
+// of a slot are a row of d / 2 bytes whose order serves the attention kernel's
+// shared-memory reads, a thread there being (g, t), g = lane / 4, t = lane % 4:
+//   K: channel 64 q + 16 t + e (e < 16) is nibble e of the 8-byte unit t (d / 64) + q,
+//      so that thread t's codes of a slot are contiguous; slot k is row
+//      k ^ (bit 2 of k) (128 / d): the slots that a load takes at once differ in
+//      bit 2, and their rows then lie in different banks.
+//   V: channel 64 q + 8 g + e (e < 8) is nibble e of the 4-byte unit g (d / 64) + q;
+//      at d = 128 the slots with bit 1 set swap the two halves of their row (banks).
+#pragma once
+
+#include <cstdint>
+
+namespace attn {
+namespace q4 {
+
+constexpr int GROUP = 64;
+constexpr int BLOCK = 64;                       // slots per block
+constexpr uint32_t BAD_WORD = 0x7FC0u;          // a group that cannot be quantised
+
+__host__ __device__ constexpr int block_bytes(int d_k, int d_v) { return 34 * (d_k + d_v); }
+__host__ __device__ constexpr int k_words_off(int d_k) { return 32 * d_k; }
+__host__ __device__ constexpr int v_off(int d_k) { return 34 * d_k; }
+__host__ __device__ constexpr int v_words_off(int d_k, int d_v) { return 34 * d_k + 32 * d_v; }
+
+// Row of slot k (0..63) in the K codes.
+__host__ __device__ constexpr int k_row(int k, int d) { return k ^ (((k >> 2) & 1) * (128 / d)); }
+
+// Byte offset, inside the K (or V) codes, of the four bytes that hold channels
+// 64 q + 8 c .. + 7 of slot k.
+__host__ __device__ constexpr int k_code_off(int k, int q, int c, int d)
+{
+    return k_row(k, d) * (d / 2) + ((c >> 1) * (d / GROUP) + q) * 8 + (c & 1) * 4;
+}
+__host__ __device__ constexpr int v_code_off(int k, int q, int c, int d)
+{
+    return k * (d / 2) + (d == 128 ? (c ^ (((k >> 1) & 1) * 4)) : c) * (4 * (d / GROUP)) + q * 4;
+}
+
+}  // namespace q4
+}  // namespace attn

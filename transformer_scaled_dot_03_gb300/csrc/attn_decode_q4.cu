@@ -1,0 +1,21 @@
+// attn_decode_q4.cu -- instantiations of the few-row attention over a cache held in 4 bits.
+#include "attn_kernel_decode_q4.cuh"
+
+namespace attn {
+
+template <int DK, int DV>
+static cudaError_t launch_rows(const DecodeQ4Params& p, cudaStream_t stream)
+{
+    return decode_q4_tile_rows(p.R) == 8 ? dq4::launch<DK, DV, 1>(p, stream) : dq4::launch<DK, DV, 2>(p, stream);
+}
+
+cudaError_t launch_decode_q4(int d_k, int d_v, const DecodeQ4Params& p, cudaStream_t stream)
+{
+    if (d_k == 64 && d_v == 64) return launch_rows<64, 64>(p, stream);
+    if (d_k == 128 && d_v == 128) return launch_rows<128, 128>(p, stream);
+    if (d_k == 64 && d_v == 128) return launch_rows<64, 128>(p, stream);
+    if (d_k == 128 && d_v == 64) return launch_rows<128, 64>(p, stream);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace attn

@@ -139,6 +139,67 @@ struct DecodeParams {
 cudaError_t launch_decode(int d_k, int d_v, int rows, const CUtensorMap& tmK, const CUtensorMap& tmV,
                           const DecodeParams& p, cudaStream_t stream);
 
+// A key/value cache held in 4 bits (format: attn_cache_q4.cuh).
+struct CacheQ4WriteParams {
+    const uint16_t* K;            // bf16 [B,H,n,d_k], H the cache's heads
+    const uint16_t* V;            // bf16 [B,H,n,d_v]
+    int H, n, m;
+    int d_k, d_v;
+    int blocks;                   // ceil(m / 64)
+    uint32_t k_groups, groups;    // groups of 64 channels in K, and in K and V
+    const int32_t* starts;        // device int32 [B] or null (0)
+    const int32_t* counts;        // device int32 [B] or null (n)
+    uint8_t* cache;
+};
+
+struct CacheQ4ReadParams {
+    const uint8_t* cache;
+    int B, H, H_kv, group;        // group = H / H_kv
+    int m, first, n, tiles;       // tiles = ceil(n / 64)
+    int d_k, d_v;
+    int blocks;
+    const int32_t* key_lengths;   // device int32 [B] or null (m)
+    uint16_t* K;                  // bf16 [B,H,n,d_k]
+    uint16_t* V;                  // bf16 [B,H,n,d_v]
+};
+
+cudaError_t launch_cache_q4_write(const CacheQ4WriteParams& p, cudaStream_t stream);
+cudaError_t launch_cache_q4_read(const CacheQ4ReadParams& p, cudaStream_t stream);
+
+// Few-row attention over that cache (attn_kernel_decode_q4.cuh).
+struct DecodeQ4Params {
+    const uint16_t* Q;            // bf16 [B,H_kv,R,d_k]: the R = group * n rows that share a cache head
+    const uint8_t* cache;
+    int B, H_kv, n, m;
+    int R;                        // rows per cache head (row r: query head r / n of the group, row r % n of it)
+    int row_tiles;                // ceil(R / rows per tile)
+    int blocks;                   // ceil(m / 64): blocks per (b, cache head)
+    int mask;
+    const int32_t* key_lengths;   // device int32 [B] (key-padding masks only)
+    const float* slopes;          // fp32 [H]: distance-bias slope per query head, or null
+    float scale_log2;             // scale * log2(e)
+    int split;                    // 1: equal shares of all blocks per CTA, parts merged after; 0: a CTA per (b, head, tile)
+    int ctas;                     // grid size
+    uint16_t* O;                  // bf16 [B,H,n,d_v]
+    float* LSE;                   // fp32 [B,H,n] or null
+    float* part_o;                // fp32 [2 ctas][part_rows][d_v] (split)
+    float* part_ml;               // fp32 [2 ctas][part_rows][2]: max (log2 domain), sum
+    int2* part_flags;             // [ctas]: the pair whose first part slot 1 holds (or -1); whether slot 0 ends its pair
+    int part_rows;
+    uint32_t* status;
+    uint64_t watchdog_ns;
+    uint32_t debug_flags;
+};
+
+// Rows per row tile of the kernel that serves R rows per cache head, and its CTAs per SM.
+__host__ __device__ constexpr int decode_q4_tile_rows(int R) { return R <= 8 ? 8 : 16; }
+__host__ __device__ constexpr int decode_q4_ctas_per_sm(int d_k, int d_v, int tile_rows)
+{
+    return tile_rows == 8 ? 3 : 2;
+}
+
+cudaError_t launch_decode_q4(int d_k, int d_v, const DecodeQ4Params& p, cudaStream_t stream);
+
 // Projections around the attention (attn_kernel_proj.cuh): Y = A Wᵀ (+ bias).
 struct ProjParams {
     int R, N, K;                  // rows (B*n), output columns, reduction length
