@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -54,6 +55,8 @@ class AttnError(RuntimeError):
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load the shared library (built by ``transformer_scaled_dot_03_gb300.build``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -396,12 +399,22 @@ def merge_proj(O: torch.Tensor, W_o: torch.Tensor, bias: torch.Tensor | None = N
     return Y
 
 
+class _Here:
+    """The current device's current stream, as a context."""
+    __slots__ = ("handle",)
+
+    def __init__(self, handle):
+        self.handle = handle
+
+    def __enter__(self):
+        return self.handle
+
+    def __exit__(self, *exc):
+        return None
+
+
 @contextlib.contextmanager
-def _on(device, stream):
-    """Run on ``device`` and ``stream`` (a torch stream, a cudaStream_t as an int, or None
-    for the device's current stream); yields the stream's handle. What is allocated
-    inside belongs to that stream, so that its memory is not handed on while a kernel
-    there still uses it."""
+def _there(device, stream):
     with torch.cuda.device(device):
         if stream is None:
             yield int(torch.cuda.current_stream().cuda_stream)
@@ -410,6 +423,17 @@ def _on(device, stream):
             stream = torch.cuda.ExternalStream(int(stream), device=device)
         with torch.cuda.stream(stream):
             yield int(stream.cuda_stream)
+
+
+def _on(device, stream):
+    """Run on ``device`` and ``stream`` (a torch stream, a cudaStream_t as an int, or None
+    for the device's current stream); yields the stream's handle. What is allocated
+    inside belongs to that stream, so that its memory is not handed on while a kernel
+    there still uses it. (The ordinary case, the current device and stream, switches
+    nothing: torch's own context managers take 5 us of the host's time, twice a short call's.)"""
+    if stream is None and device.index == torch.cuda.current_device():
+        return _Here(torch._C._cuda_getCurrentRawStream(device.index))
+    return _there(device, stream)
 
 
 def _cuda_arg(name, t, dtype, shape, device):
@@ -458,8 +482,9 @@ def cache_q4_write(cache: torch.Tensor, K: torch.Tensor, V: torch.Tensor, starts
         if t is not None:
             _cuda_arg(name, t, torch.int32, (B,), dev)
     with _on(dev, stream) as handle:
-        rc = load().attn_cache_q4_write(_ptr(K), _ptr(V), B, H_kv, n, m, d_k, d_v, _ptr(starts), _ptr(counts),
-                                        _ptr(cache), ctypes.c_void_p(handle))
+        rc = load().attn_cache_q4_write(K.data_ptr(), V.data_ptr(), B, H_kv, n, m, d_k, d_v,
+                                        None if starts is None else starts.data_ptr(),
+                                        None if counts is None else counts.data_ptr(), cache.data_ptr(), handle)
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_cache_q4_write", last_error() if rc == ATTN_ERR_CUDA else "")
     return cache
@@ -486,13 +511,15 @@ def cache_q4_read(cache: torch.Tensor, d_k: int, m: int | None = None, key_lengt
     with _on(dev, stream) as handle:
         K = torch.empty((B, H, n, d_k), dtype=torch.bfloat16, device=dev) if K is None else K
         V = torch.empty((B, H, n, d_v), dtype=torch.bfloat16, device=dev) if V is None else V
-        rc = load().attn_cache_q4_read(_ptr(cache), B, H, H_kv, m, int(first), n, d_k, d_v, _ptr(key_lengths), _ptr(K),
-                                       _ptr(V), ctypes.c_void_p(handle))
+        rc = load().attn_cache_q4_read(cache.data_ptr(), B, H, H_kv, m, int(first), n, d_k, d_v,
+                                       None if key_lengths is None else key_lengths.data_ptr(), K.data_ptr(),
+                                       V.data_ptr(), handle)
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_cache_q4_read", last_error() if rc == ATTN_ERR_CUDA else "")
     return K, V
 
 
+@functools.lru_cache(maxsize=256)          # a function of the sizes alone
 def decode_q4_workspace_size(B, H, H_kv, n, m, d_k, d_v) -> int:
     return int(load().attn_decode_q4_workspace_size(int(B), int(H), int(H_kv), int(n), int(m), int(d_k), int(d_v)))
 
@@ -536,11 +563,13 @@ def decode_q4(Q: torch.Tensor, cache: torch.Tensor, mask: str = "none", key_leng
             LSE = torch.empty((B, H, n), dtype=torch.float32, device=dev)
         if workspace is None and ws_bytes > 0:
             workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-        rc = load().attn_decode_q4(_ptr(Q), _ptr(cache), B, H, H_kv, n, m, d_k, d_v, MASK_CODES[mask],
-                                   _ptr(key_lengths) if uses_lengths else None, _ptr(slopes),
-                                   ctypes.c_float(-1.0 if scale is None else float(scale)), _ptr(O), _ptr(LSE),
-                                   _ptr(workspace), ctypes.c_size_t(0 if workspace is None else workspace.numel()),
-                                   ctypes.c_void_p(handle))
+        rc = load().attn_decode_q4(Q.data_ptr(), cache.data_ptr(), B, H, H_kv, n, m, d_k, d_v, MASK_CODES[mask],
+                                   key_lengths.data_ptr() if uses_lengths else None,
+                                   None if slopes is None else slopes.data_ptr(),
+                                   -1.0 if scale is None else float(scale), O.data_ptr(),
+                                   None if LSE is None else LSE.data_ptr(),
+                                   None if workspace is None else workspace.data_ptr(),
+                                   0 if workspace is None else workspace.numel(), handle)
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_decode_q4", last_error() if rc == ATTN_ERR_CUDA else "")
     return O, LSE

@@ -971,8 +971,10 @@ extern "C" int attn_merge_proj(const void* O, const void* W_o, const void* bias,
 namespace {
 
 constexpr int kQ4MaxRows = 64;            // rows per cache head up to which the few-row kernel runs
-constexpr int64_t kQ4MaxCtas = 1024;      // bound on its split grid, used to size the workspace
-constexpr int kQ4SplitBlocks = 16;        // more blocks than this per (b, cache head) are split over CTAs
+constexpr int kQ4WholeBlocks = 2;         // up to this many blocks per (b, cache head) a warp takes whole pairs
+
+// Bound on the kernel's warps, used to size the workspace.
+int64_t q4_max_warps(int tile_rows) { return tile_rows == 8 ? 2048 : 1280; }
 
 // Sizes that every entry point on the cache shares.
 int q4_validate(int B, int H_kv, int m, int d_k, int d_v)
@@ -989,9 +991,9 @@ int q4_blocks(int m) { return static_cast<int>((static_cast<int64_t>(m) + attn::
 struct Q4Plan {
     bool few, split;
     int rows, row_tiles;              // rows per cache head, tiles of them
-    int64_t pairs, ctas;              // (b, cache head, row tile) triples; largest split grid
+    int64_t pairs, warps;             // (b, cache head, row tile) triples; most workers
     int part_rows;
-    size_t ml_off, flags_off;         // split
+    size_t ml_off, first_off, ends_off;   // split
     size_t v_off;                     // many rows
     size_t total;
 };
@@ -1011,14 +1013,15 @@ Q4Plan q4_plan(int64_t B, int64_t H, int64_t H_kv, int64_t n, int m, int d_k, in
     w.row_tiles = (w.rows + tile - 1) / tile;
     w.pairs = B * H_kv * w.row_tiles;
     const int64_t blocks = q4_blocks(m);
-    w.split = blocks > kQ4SplitBlocks;
+    w.split = blocks > kQ4WholeBlocks;
+    w.warps = std::min(q4_max_warps(tile), w.split ? w.pairs * blocks : w.pairs);
     if (!w.split) return w;
-    w.ctas = std::max<int64_t>(1, std::min(kQ4MaxCtas, w.pairs * blocks / 4));
     w.part_rows = std::min(w.rows, tile);
-    const size_t parts = static_cast<size_t>(2 * w.ctas) * w.part_rows;
+    const size_t parts = static_cast<size_t>(2 * w.warps) * w.part_rows;
     w.ml_off = round_up(parts * d_v * 4, kWsAlign);
-    w.flags_off = w.ml_off + round_up(parts * 2 * 4, kWsAlign);
-    w.total = w.flags_off + round_up(static_cast<size_t>(w.ctas) * 8, kWsAlign);
+    w.first_off = w.ml_off + round_up(parts * 2 * 4, kWsAlign);
+    w.ends_off = w.first_off + round_up(static_cast<size_t>(w.pairs) * 4, kWsAlign);
+    w.total = w.ends_off + round_up(static_cast<size_t>(w.warps) * 4, kWsAlign);
     return w;
 }
 
@@ -1163,19 +1166,17 @@ extern "C" int attn_decode_q4(const void* Q, const void* cache, int B, int H, in
     p.slopes = slopes;
     p.scale_log2 = static_cast<float>(sc * 1.4426950408889634074);
     p.split = w.split ? 1 : 0;
-    p.ctas = static_cast<int>(w.pairs);
-    if (w.split) {
-        int num_sms = 0;
-        if ((rc = sm_count(&num_sms)) != ATTN_OK) return rc;
-        const int64_t slots = static_cast<int64_t>(num_sms) *
-                              attn::decode_q4_ctas_per_sm(d_k, d_v, attn::decode_q4_tile_rows(w.rows));
-        p.ctas = static_cast<int>(std::min(slots, w.ctas));
-    }
+    int num_sms = 0;
+    if ((rc = sm_count(&num_sms)) != ATTN_OK) return rc;
+    p.warps = static_cast<int>(std::min<int64_t>(
+        w.warps, static_cast<int64_t>(num_sms) * 4 *
+                     attn::decode_q4_ctas_per_sm(d_k, d_v, attn::decode_q4_tile_rows(w.rows))));
     p.O = static_cast<uint16_t*>(O);
     p.LSE = LSE;
     p.part_o = reinterpret_cast<float*>(wsb);
     p.part_ml = reinterpret_cast<float*>(wsb + w.ml_off);
-    p.part_flags = reinterpret_cast<int2*>(wsb + w.flags_off);
+    p.pair_first = reinterpret_cast<int*>(wsb + w.first_off);
+    p.part_ends = reinterpret_cast<int*>(wsb + w.ends_off);
     p.part_rows = w.part_rows;
     p.status = status;
     p.watchdog_ns = g_watchdog_ns;

@@ -178,13 +178,14 @@ struct DecodeQ4Params {
     const int32_t* key_lengths;   // device int32 [B] (key-padding masks only)
     const float* slopes;          // fp32 [H]: distance-bias slope per query head, or null
     float scale_log2;             // scale * log2(e)
-    int split;                    // 1: equal shares of all blocks per CTA, parts merged after; 0: a CTA per (b, head, tile)
-    int ctas;                     // grid size
+    int split;                    // 1: equal shares of all blocks per warp, parts merged after; 0: whole pairs
+    int warps;                    // workers
     uint16_t* O;                  // bf16 [B,H,n,d_v]
     float* LSE;                   // fp32 [B,H,n] or null
-    float* part_o;                // fp32 [2 ctas][part_rows][d_v] (split)
-    float* part_ml;               // fp32 [2 ctas][part_rows][2]: max (log2 domain), sum
-    int2* part_flags;             // [ctas]: the pair whose first part slot 1 holds (or -1); whether slot 0 ends its pair
+    float* part_o;                // fp32 [2 warps][part_rows][d_v] (split)
+    float* part_ml;               // fp32 [2 warps][part_rows][2]: max (log2 domain), sum
+    int* pair_first;              // [pairs]: the worker whose slot 1 holds a cut pair's first part, -1 for a whole pair
+    int* part_ends;               // [warps]: whether the worker's slot 0 is the last part of its pair
     int part_rows;
     uint32_t* status;
     uint64_t watchdog_ns;

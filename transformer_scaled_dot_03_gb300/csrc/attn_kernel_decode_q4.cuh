@@ -15,26 +15,31 @@
 // u 2^-24; the next nibble, masked in place, is u 2^-20. So a word of eight codes
 // becomes four operand registers with four ANDs and one shift, exactly and without an
 // offset to take out again. The fp16 partner carries the scales: the query row times a
-// power of two that brings its largest magnitude to [2^14, 2^15) (and 2^-4 for the
+// power of two that brings its largest magnitude to [2^8, 2^9) (and 2^-4 for the
 // odd nibbles), for V the weights p s R, R a power of two per group and warp that
 // keeps the largest s R in [2^12, 2^15).
 //
 //   scores   S^T[slot][row] = s (sum_c u_c q_c - u0 sum_c q_c), summed over the groups
 //   output   O^T[c][row]    = sum_j (p_j s_j R) u_jc - sum_j (p_j s_j R) u0_j, over R l
 //
+// The zeros are nibbles too, and both terms with u0 are one more product each: for the
+// scores A holds the u0 of a slot's groups and B -sum_c q_c (as the sum of two fp16), for
+// the output A holds the slots' u0 in every row.
+//
 // The scores' accumulator has a slot in its row and two query rows in its columns; the
 // weights go to the second product's B operand through movmatrix (an 8 x 8 transpose
 // in registers). Row r of a 16-slot tile is slot 4 (r % 2) + (r % 8) / 2 + 8 (r / 8), so that
 // a thread's four V slots are t, t + 4, t + 8, t + 12 and a warp reads 16 contiguous rows.
 //
-// A warp streams its own blocks through its own ring (lane 0 issues a bulk copy per
-// block as soon as the warp has consumed the stage) with an online softmax of its own;
-// the CTA's warps share one (b, cache head, row tile) at a time, block by block, and
-// merge at its end. With `split` the blocks of all pairs, as the entries' lengths have
-// them on the device, are dealt out evenly: CTA c takes units [T c / G, T (c + 1) / G). A
-// pair that lies in one CTA is written there; of one that is cut, each CTA writes its
-// part (max, sum, unnormalised O) to its slot 0 (the pair began in an earlier CTA) or
-// slot 1, and a second kernel merges the parts in order.
+// Every warp is a worker of its own: the blocks of all (entry, cache head, row tile)
+// pairs, as the entries' lengths have them on the device, form one sequence, and of T
+// blocks warp w of W takes [T w / W, T (w + 1) / W), streaming them through its own ring
+// (lane 0 issues a bulk copy per block as soon as the warp has consumed a stage, across
+// the pairs' ends) with an online softmax of its own. A pair that lies in one warp's
+// range is written there; of one that is cut, each warp writes its part (max, sum,
+// unnormalised O) to its slot 0 (the pair began in an earlier warp) or slot 1, and a
+// second kernel merges the parts in order. (A CTA per pair, its warps merging in
+// shared memory, spent 6 us per pair on latencies that nothing covered.)
 #pragma once
 
 #include <cstdint>
@@ -64,13 +69,19 @@ struct Layout {
     // 2 blocks of 8704 or 6528 bytes, or 3 of 4352, in flight per warp
     static constexpr int STAGES = DK + DV == 128 ? 3 : 2;
     static constexpr int RING = WARPS * STAGES * BYTES_BLOCK;
-    // the merge of the warps reuses the ring: per warp max and sum [ROWS], O [ROWS][DV]
-    static constexpr int RED_WARP = ROWS * (DV + 2);
-    static_assert(WARPS * RED_WARP * 4 <= RING, "merge area inside the ring");
-    static constexpr int BAR_OFF = RING;
+    static constexpr int ROW_OFF = RING;                  // per warp and row: RowInfo
+    static constexpr int BAR_OFF = ROW_OFF + WARPS * ROWS * 16;
     static constexpr int MISC_OFF = BAR_OFF + (WARPS * STAGES + 1) * 8;
     static constexpr int BYTES = MISC_OFF + 16 + 128;
     static_assert(BYTES * decode_q4_ctas_per_sm(DK, DV, ROWS) <= 232448 - 3 * 1024, "shared memory budget");
+};
+
+// What the masks and the distance bias need to know of a query row.
+struct __align__(16) RowInfo {
+    int lim;        // slots below it are visible
+    int pos;        // its position among the slots
+    float slope;    // of its head, log2 domain
+    float fac;      // raw scores to the log2 domain
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -80,6 +91,22 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same onto an accumulator of zeros, half of A (k >= 8) and of B being zero.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %7, %7}, {%6, %7}, {%8, %8, %8, %8};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(b0), "r"(0u), "f"(0.f));
+}
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
 }
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t a)
@@ -101,12 +128,8 @@ __device__ __forceinline__ float pow2i(int e) { return __uint_as_float(static_ca
 // Exponent of a finite positive x (subnormals: -127).
 __device__ __forceinline__ int exponent(float x) { return static_cast<int>((__float_as_uint(x) >> 23) & 255u) - 127; }
 
-// Step and zero of a group word in the lower half of w.
-__device__ __forceinline__ float word_step(uint32_t w) { return __uint_as_float((w << 16) & 0xFFF00000u); }
-__device__ __forceinline__ float word_zero(uint32_t w)
-{
-    return __uint_as_float(((w << 19) & 0x00780000u) | 0x41800000u) - 16.f;   // (16 + u0) - 16
-}
+// Step of group q in a slot's words (u0, in the low bits, masked off).
+__device__ __forceinline__ float word_step(uint32_t w, int q) { return __uint_as_float((q ? w : w << 16) & 0xFFF00000u); }
 
 // The slots of entry b that some row sees end here; kv_len: its filled slots.
 __device__ __forceinline__ int visible_end(const DecodeQ4Params& p, int b, int* kv_len)
@@ -129,6 +152,88 @@ __device__ __forceinline__ int pair_blocks(const DecodeQ4Params& p, int b)
     return max(1, (visible_end(p, b, &kv) + q4::BLOCK - 1) / q4::BLOCK);
 }
 
+// A place in the sequence of blocks: block blk of nb of pair pr of entry b, and the
+// units left to take (blocks, or whole pairs without `split`).
+struct Cursor {
+    int b, pr, blk, nb, todo;
+
+    __device__ __forceinline__ void next(const DecodeQ4Params& p, int pairs_b)
+    {
+        if (p.split) --todo;
+        if (++blk < nb) return;
+        if (!p.split) --todo;
+        blk = 0;
+        if (++pr == pairs_b) {
+            pr = 0;
+            ++b;
+            if (todo > 0) nb = pair_blocks(p, b);
+        }
+    }
+};
+
+// Warp w's share of the sequence.
+__device__ __forceinline__ Cursor first_block(const DecodeQ4Params& p, int w, int lane, int pairs_b)
+{
+    Cursor c;
+    if (!p.split) {
+        const int64_t pairs = static_cast<int64_t>(p.B) * pairs_b;
+        const int64_t p0 = pairs * w / p.warps;
+        c.todo = static_cast<int>(pairs * (w + 1) / p.warps - p0);
+        c.b = static_cast<int>(p0 / pairs_b);
+        c.pr = static_cast<int>(p0 - static_cast<int64_t>(c.b) * pairs_b);
+        c.blk = 0;
+        c.nb = c.todo > 0 ? pair_blocks(p, c.b) : 1;
+        return c;
+    }
+    const bool ragged = mask_has_lengths(p.mask);
+    int64_t total;
+    if (ragged) {
+        int64_t sum = 0;
+        for (int i = lane; i < p.B; i += 32) sum += pair_blocks(p, i);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        total = sum * pairs_b;
+    } else {
+        total = static_cast<int64_t>(p.B) * pairs_b * pair_blocks(p, 0);
+    }
+    const int64_t warps = min(static_cast<int64_t>(p.warps), total);
+    const int64_t u0 = total * min(static_cast<int64_t>(w), warps) / warps;
+    const int64_t u1 = total * min(static_cast<int64_t>(w) + 1, warps) / warps;
+    c.todo = static_cast<int>(u1 - u0);
+    c.b = c.pr = c.blk = 0;
+    c.nb = 1;
+    if (c.todo == 0) return c;
+    int64_t before = 0;                                  // units of the entries before b
+    if (ragged) {
+        for (int base = 0; base < p.B; base += 32) {
+            const int64_t nb = base + lane < p.B ? static_cast<int64_t>(pair_blocks(p, base + lane)) * pairs_b : 0;
+            int64_t incl = nb;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int64_t v = __shfl_up_sync(0xffffffffu, incl, off);
+                if (lane >= off) incl += v;
+            }
+            const uint32_t past = __ballot_sync(0xffffffffu, before + incl > u0);
+            if (past != 0u) {
+                const int l = __ffs(past) - 1;
+                c.b = base + l;
+                before += __shfl_sync(0xffffffffu, incl - nb, l);
+                break;
+            }
+            before += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        c.nb = pair_blocks(p, c.b);
+    } else {
+        c.nb = pair_blocks(p, 0);
+        const int64_t per = static_cast<int64_t>(pairs_b) * c.nb;
+        c.b = static_cast<int>(u0 / per);
+        before = per * c.b;
+    }
+    c.pr = static_cast<int>((u0 - before) / c.nb);
+    c.blk = static_cast<int>((u0 - before) - static_cast<int64_t>(c.pr) * c.nb);
+    return c;
+}
+
 template <int DK, int DV, int NT>
 __global__ void __launch_bounds__(THREADS, decode_q4_ctas_per_sm(DK, DV, 8 * NT))
 attn_decode_q4_kernel(const DecodeQ4Params p)
@@ -140,9 +245,11 @@ attn_decode_q4_kernel(const DecodeQ4Params p)
     const uint32_t sbase = smem_u32(smem);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int g = lane >> 2, t = lane & 3;
-    const uint32_t bar0 = sbase + L::BAR_OFF + 8u * static_cast<uint32_t>(warp * L::STAGES);   // this warp's ring
+    const uint32_t ring = sbase + static_cast<uint32_t>(warp * L::STAGES * L::BYTES_BLOCK);    // this warp's
+    const uint32_t bar0 = sbase + L::BAR_OFF + 8u * static_cast<uint32_t>(warp * L::STAGES);
     const uint32_t bar_never = sbase + L::BAR_OFF + 8u * static_cast<uint32_t>(WARPS * L::STAGES);
     volatile uint32_t* abort_word = reinterpret_cast<volatile uint32_t*>(smem + L::MISC_OFF);
+    RowInfo* info = reinterpret_cast<RowInfo*>(smem + L::ROW_OFF) + warp * L::ROWS;
     if (threadIdx.x == 0) {
         for (int s = 0; s < WARPS * L::STAGES + 1; ++s) mbar_init(sbase + L::BAR_OFF + 8u * s, 1);
         *abort_word = 0u;
@@ -151,109 +258,57 @@ attn_decode_q4_kernel(const DecodeQ4Params p)
     __syncthreads();
     griddep_wait();   // the previous grid's writes (Q, the cache, the lengths) are visible
 
-    // ------------------------------------------------ this CTA's units
-    const int cta = static_cast<int>(blockIdx.x);
+    // consecutive workers sit in different CTAs, so that little work spreads over the SMs
+    const int worker = warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+    if (worker >= p.warps) return;
     const int pairs_b = p.H_kv * p.row_tiles;            // pairs per entry
-    int b = 0, pr = 0, blk = 0;                          // entry, pair inside it, first block
-    int64_t todo;                                        // units to take
-    bool mid_pair = false;                               // the first segment began in an earlier CTA
-    if (!p.split) {
-        b = cta / pairs_b;
-        pr = cta - b * pairs_b;
-        todo = pair_blocks(p, b);
-    } else {
-        int64_t total;
-        const bool ragged = mask_has_lengths(p.mask);
-        if (ragged) {
-            int64_t sum = 0;
-            for (int i = lane; i < p.B; i += 32) sum += pair_blocks(p, i);
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-            total = sum * pairs_b;
-        } else {
-            total = static_cast<int64_t>(p.B) * pairs_b * pair_blocks(p, 0);
+    Cursor at = first_block(p, worker, lane, pairs_b);
+    Cursor ahead = at;                                   // the next block to copy
+    uint32_t landed = 0, issued = 0;                     // blocks consumed, copies issued
+    auto issue = [&]() {
+        const int64_t block = (static_cast<int64_t>(ahead.b) * p.H_kv + ahead.pr / p.row_tiles) * p.blocks + ahead.blk;
+        if (lane == 0) {
+            const uint32_t s = issued % L::STAGES;
+            mbar_arrive_expect_tx(bar0 + 8u * s, L::BYTES_BLOCK);
+            bulk_load(ring + s * L::BYTES_BLOCK, p.cache + block * L::BYTES_BLOCK, L::BYTES_BLOCK, bar0 + 8u * s);
         }
-        // at least one block per warp
-        const int64_t ctas = max(static_cast<int64_t>(1), min(static_cast<int64_t>(p.ctas), total / WARPS));
-        if (cta >= ctas) {
-            if (threadIdx.x == 0) p.part_flags[cta] = make_int2(-1, 0);
-            return;
-        }
-        const int64_t u0 = total * cta / ctas, u1 = total * (cta + 1) / ctas;
-        todo = u1 - u0;
-        int64_t before = 0;                              // units of the entries before b
-        if (ragged) {
-            for (int base = 0; base < p.B; base += 32) {
-                const int64_t nb = base + lane < p.B ? static_cast<int64_t>(pair_blocks(p, base + lane)) * pairs_b : 0;
-                int64_t incl = nb;
-#pragma unroll
-                for (int off = 1; off < 32; off <<= 1) {
-                    const int64_t v = __shfl_up_sync(0xffffffffu, incl, off);
-                    if (lane >= off) incl += v;
-                }
-                const uint32_t past = __ballot_sync(0xffffffffu, before + incl > u0);
-                if (past != 0u) {
-                    const int l = __ffs(past) - 1;
-                    b = base + l;
-                    before += __shfl_sync(0xffffffffu, incl - nb, l);
-                    break;
-                }
-                before += __shfl_sync(0xffffffffu, incl, 31);
-            }
-        } else {
-            const int64_t per = static_cast<int64_t>(pairs_b) * pair_blocks(p, 0);
-            b = static_cast<int>(u0 / per);
-            before = per * b;
-        }
-        const int nb = pair_blocks(p, b);
-        pr = static_cast<int>((u0 - before) / nb);
-        blk = static_cast<int>((u0 - before) - static_cast<int64_t>(pr) * nb);
-        mid_pair = blk > 0;
-    }
-
+        ++issued;
+        ahead.next(p, pairs_b);
+    };
     bool ok = true;
     if (p.debug_flags & DEBUG_FORCE_TIMEOUT) {
         ok = mbar_wait(bar_never, 0, abort_word, p.status, STATUS_FORCED, 20000000ull);
         ok = __all_sync(0xffffffffu, ok);
     }
-    uint32_t landed = 0;                                 // blocks this warp has waited for, over all segments
-    int tail_pair = -1, head_end = 0;
+    if (ok)
+        while (issued < L::STAGES && ahead.todo > 0) issue();
+
     const int pi = 4 * (g & 1) + (g >> 1);               // slot of tile row g inside a 16-slot tile
     // byte offsets of this thread's codes and words inside a block
     const int k_lo = q4::k_row(pi, DK) * (DK / 2) + t * 8 * NGK, k_hi = q4::k_row(pi + 8, DK) * (DK / 2) + t * 8 * NGK;
     const int v_0 = q4::v_off(DK) + q4::v_code_off(t, 0, g, DV);
-    const int w_lo = 2 * NGK * pi, vw_lo = 2 * NGV * pi;
+    const int kw_0 = q4::k_words_off(DK) + 2 * NGK * pi, vw_0 = q4::v_words_off(DK, DV) + 2 * NGV * pi;
+    const int vz_0 = q4::v_words_off(DK, DV) + 2 * NGV * t;
+    const bool biased = p.slopes != nullptr;
+    int head_end = 0;
 
-    while (todo > 0) {
+    while (ok && at.todo > 0) {
+        // -------------------------------------------- a pair (or this warp's part of one)
+        const bool mid_pair = at.blk > 0;                // it began in an earlier warp
+        const int hk = at.pr / p.row_tiles, rt = at.pr - hk * p.row_tiles;
+        const int64_t pair_bh = static_cast<int64_t>(at.b) * p.H_kv + hk;
+        const int64_t pair = pair_bh * p.row_tiles + rt;
+        const int nb = at.nb;
+        const int last = p.split ? min(nb, at.blk + at.todo) : nb;   // one past its last block here
         int kv_len;
-        const int end = visible_end(p, b, &kv_len);      // slots past it are seen by no row
-        const int nb = max(1, (end + q4::BLOCK - 1) / q4::BLOCK);
-        const int take = static_cast<int>(min(static_cast<int64_t>(nb - blk), todo));
-        const int hk = pr / p.row_tiles, rt = pr - hk * p.row_tiles;
-        const int64_t pair_bh = static_cast<int64_t>(b) * p.H_kv + hk;
-        const uint8_t* src = p.cache + (pair_bh * p.blocks + blk) * L::BYTES_BLOCK;
-        const int mine = take > warp ? (take - warp + WARPS - 1) / WARPS : 0;   // blocks warp, warp + 4, ...
-        const int count = end > 0 ? mine : 0;
-        auto issue = [&](int i) {                        // block i of this warp into its stage
-            const uint32_t s = (landed + static_cast<uint32_t>(i)) % L::STAGES;
-            mbar_arrive_expect_tx(bar0 + 8u * s, L::BYTES_BLOCK);
-            bulk_load(sbase + (warp * L::STAGES + s) * L::BYTES_BLOCK, src + static_cast<int64_t>(warp + WARPS * i) * L::BYTES_BLOCK,
-                      L::BYTES_BLOCK, bar0 + 8u * s);
-        };
-        int issued = 0;
-        if (ok) {
-            issued = min(count, L::STAGES);
-            if (lane == 0)
-                for (int i = 0; i < issued; ++i) issue(i);
-        }
-
-        // -------------------------------------------- the query rows, as fp16 B operands
-        uint32_t bq[NT][NGK][4][2];
-        float sq[NT][2][NGK], fac[NT][2];
-        float slope[NT][2];
-        int lim[NT][2], pos[NT][2];
-        const int r0 = rt * L::ROWS;
+        const int end = visible_end(p, at.b, &kv_len);   // slots past it are seen by no row
         const int off = causal_offset(p.mask, p.m - p.n, kv_len, p.n);
+        const int r0 = rt * L::ROWS;
+        const int rows = min(L::ROWS, p.R - r0);
+
+        // the query rows, as fp16 B operands
+        uint32_t bq[NT][NGK][4][2], bz[NT][NGK];
+        float ef[NT][2];                                 // raw scores to the log2 domain
         int min_lim = end;                               // every row sees the slots below it
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -270,119 +325,121 @@ attn_decode_q4_kernel(const DecodeQ4Params p)
                     qv[q][0] = x.x; qv[q][1] = x.y; qv[q][2] = x.z; qv[q][3] = x.w;
                     qv[q][4] = y.x; qv[q][5] = y.y; qv[q][6] = y.z; qv[q][7] = y.w;
                 }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) top = max(top, max(qv[q][i] & 0x7FFFu, (qv[q][i] >> 16) & 0x7FFFu));
             }
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // 2^e q has its largest magnitude in [2^14, 2^15); an infinity or NaN stays one
-            const int e = max(-113, min(110, 14 - (static_cast<int>(top >> 7) - 127)));
-            const float up = pow2i(e);
-            float sum[NGK];
+            {
+                // the row's mask and bias, while the loads are under way
+                const int i = r % p.n;
+                RowInfo ri;
+                ri.pos = i + off;
+                ri.lim = mask_is_causal(p.mask) ? min(kv_len, i + off + 1) : kv_len;
+                ri.slope = biased && r < p.R ? __ldg(p.slopes + hk * (p.R / p.n) + r / p.n) * LOG2E : 0.f;
+                min_lim = min(min_lim, ri.lim);
 #pragma unroll
-            for (int q = 0; q < NGK; ++q) {
-                float x[16];
-                sum[q] = 0.f;
+                for (int q = 0; q < NGK; ++q)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    x[2 * i] = __uint_as_float(qv[q][i] << 16) * up;
-                    x[2 * i + 1] = __uint_as_float(qv[q][i] & 0xFFFF0000u) * up;
-                    sum[q] += x[2 * i] + x[2 * i + 1];
-                }
-                // word w, half h: nibbles 2 h (u 2^-24) and 2 h + 1 (u 2^-20) of both 16-bit halves
+                    for (int k = 0; k < 8; ++k) top = max_u16x2(top, qv[q][k] & 0x7FFF7FFFu);
+                top = max(top & 0xFFFFu, top >> 16);
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                // 2^e q has its largest magnitude in [2^8, 2^9); an infinity or NaN stays one
+                const int e = max(-119, min(110, 8 - (static_cast<int>(top >> 7) - 127)));
+                // scale * log2(e) * 2^(24 - e), kept finite and positive
+                ri.fac = fmaxf(fminf(p.scale_log2 * pow2i(24 - max(e, -100)) * pow2i(max(0, -100 - e)), 3e38f), 1.2e-38f);
+                __syncwarp();
+                if (t == 0) info[8 * nt + g] = ri;
+                __syncwarp();
+                const float up = pow2i(e);
 #pragma unroll
-                for (int w = 0; w < 2; ++w)
+                for (int q = 0; q < NGK; ++q) {
+                    float x[16], sum = 0.f;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int c = 8 * w + 2 * h;
-                        bq[nt][q][2 * w + h][0] = pack_f16x2(x[c], x[c + 4]);
-                        bq[nt][q][2 * w + h][1] = pack_f16x2(x[c + 1] * 0.0625f, x[c + 5] * 0.0625f);
+                    for (int k = 0; k < 8; ++k) {
+                        x[2 * k] = __uint_as_float(qv[q][k] << 16) * up;
+                        x[2 * k + 1] = __uint_as_float(qv[q][k] & 0xFFFF0000u) * up;
+                        sum += x[2 * k] + x[2 * k + 1];
                     }
-                sum[q] += __shfl_xor_sync(0xffffffffu, sum[q], 1);
-                sum[q] += __shfl_xor_sync(0xffffffffu, sum[q], 2);
-            }
-            // per column of the accumulators (query rows 2 t and 2 t + 1 of this tile)
+                    // word w, half h: nibbles 2 h (u 2^-24) and 2 h + 1 (u 2^-20) of both 16-bit halves
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const int srcl = 4 * (2 * t + c);
+                    for (int w = 0; w < 2; ++w)
 #pragma unroll
-                for (int q = 0; q < NGK; ++q) sq[nt][c][q] = __shfl_sync(0xffffffffu, sum[q], srcl) * (1.f / TWO24);
-                const int ec = __shfl_sync(0xffffffffu, e, srcl);
-                // scale * log2(e) * 2^(24 - e), kept finite
-                fac[nt][c] = fminf(p.scale_log2 * pow2i(24 - max(ec, -100)) * pow2i(max(0, -100 - ec)), 3e38f);
-                const int rc = r0 + 8 * nt + 2 * t + c;
-                const int i = rc % p.n;
-                pos[nt][c] = i + off;
-                lim[nt][c] = mask_is_causal(p.mask) ? min(kv_len, i + off + 1) : kv_len;
-                slope[nt][c] = p.slopes != nullptr && rc < p.R ? __ldg(p.slopes + hk * (p.R / p.n) + rc / p.n) * LOG2E : 0.f;
-                min_lim = min(min_lim, lim[nt][c]);
+                        for (int h = 0; h < 2; ++h) {
+                            const int c = 8 * w + 2 * h;
+                            bq[nt][q][2 * w + h][0] = pack_f16x2(x[c], x[c + 4]);
+                            bq[nt][q][2 * w + h][1] = pack_f16x2(x[c + 1] * 0.0625f, x[c + 5] * 0.0625f);
+                        }
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                    // -sum q as two fp16: k = q holds the upper part, k = 2 + q the rest
+                    const uint32_t hi = pack_f16x2(-sum, 0.f);
+                    float back;
+                    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.f32.f16 %0, l;\n\t}" : "=f"(back) : "r"(hi));
+                    const uint32_t part = t == 0 ? hi : t == 1 ? pack_f16x2(-sum - back, 0.f) : 0u;
+                    bz[nt][q] = q ? part << 16 : part;
+                }
             }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) ef[nt][c] = biased ? 1.f : info[8 * nt + 2 * t + c].fac;
         }
         min_lim = __reduce_min_sync(0xffffffffu, min_lim);
-        const bool biased = p.slopes != nullptr;
 
-        float m_run[NT][2], l_run[NT][2], corr[NT][2][NGV], o[NT][NGV][4][4], rg[NGV];
+        float m_run[NT][2], l_run[NT][2], o[NT][NGV][4][4], zc[NT][4], rg[NGV];
+        uint32_t thr = 0u;                               // the words whose s R stays below 2^15, per group
 #pragma unroll
-        for (int q = 0; q < NGV; ++q) rg[q] = 0.f;       // 0: no reference yet
+        for (int q = 0; q < NGV; ++q) rg[q] = 1.f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 m_run[nt][c] = -INFINITY;
                 l_run[nt][c] = 0.f;
-#pragma unroll
-                for (int q = 0; q < NGV; ++q) corr[nt][c][q] = 0.f;
             }
 #pragma unroll
-            for (int q = 0; q < NGV; ++q)
+            for (int c = 0; c < 4; ++c) {
+                zc[nt][c] = 0.f;
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int q = 0; q < NGV; ++q)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) o[nt][q][j][c] = 0.f;
+                    for (int j = 0; j < 4; ++j) o[nt][q][j][c] = 0.f;
+            }
         }
 
-        // -------------------------------------------- the blocks
-        for (int it = 0; ok && it < count; ++it) {
+        // -------------------------------------------- its blocks
+        for (int blk = at.blk; blk < last; ++blk) {
             const uint32_t stage = landed % L::STAGES;
             ok = mbar_wait(bar0 + 8u * stage, (landed / L::STAGES) & 1u, abort_word, p.status, STATUS_SOFTMAX_WAIT,
                            p.watchdog_ns);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             const uint8_t* sb = smem + (warp * L::STAGES + stage) * L::BYTES_BLOCK;
-            const int key0 = (blk + warp + WARPS * it) * q4::BLOCK;
+            const int key0 = blk * q4::BLOCK;
             const bool masked = key0 + q4::BLOCK > min_lim;
 
-            // scores, scaled to the log2 domain
+            // raw scores
             float x[4][NT][4];
 #pragma unroll
             for (int tile = 0; tile < 4; ++tile) {
-                uint32_t lo[2 * NGK], hi[2 * NGK];
+                uint32_t lo[2 * NGK], hi[2 * NGK], wl, wh;
                 const uint8_t* kb = sb + tile * 16 * (DK / 2);
+                const uint8_t* wb = sb + kw_0 + tile * 16 * 2 * NGK;
                 if (NGK == 2) {
                     const uint4 a = *reinterpret_cast<const uint4*>(kb + k_lo), c = *reinterpret_cast<const uint4*>(kb + k_hi);
                     lo[0] = a.x; lo[1] = a.y; lo[2 * NGK - 2] = a.z; lo[2 * NGK - 1] = a.w;
                     hi[0] = c.x; hi[1] = c.y; hi[2 * NGK - 2] = c.z; hi[2 * NGK - 1] = c.w;
+                    wl = *reinterpret_cast<const uint32_t*>(wb);
+                    wh = *reinterpret_cast<const uint32_t*>(wb + 8 * 2 * NGK);
                 } else {
                     const uint2 a = *reinterpret_cast<const uint2*>(kb + k_lo), c = *reinterpret_cast<const uint2*>(kb + k_hi);
                     lo[0] = a.x; lo[1] = a.y;
                     hi[0] = c.x; hi[1] = c.y;
-                }
-                const uint8_t* wb = sb + q4::k_words_off(DK) + tile * 16 * 2 * NGK + w_lo;
-                uint32_t wl, wh;
-                if (NGK == 2) {
-                    wl = *reinterpret_cast<const uint32_t*>(wb);
-                    wh = *reinterpret_cast<const uint32_t*>(wb + 8 * 2 * NGK);
-                } else {
                     wl = *reinterpret_cast<const uint16_t*>(wb);
                     wh = *reinterpret_cast<const uint16_t*>(wb + 8 * 2 * NGK);
                 }
+                const uint32_t zl = wl & LO, zh = wh & LO;
 #pragma unroll
                 for (int q = 0; q < NGK; ++q) {
                     float acc[NT][4];
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) acc[nt][c] = 0.f;
+                    for (int nt = 0; nt < NT; ++nt) mma_f16_first(acc[nt], zl, zh, bz[nt][q]);
 #pragma unroll
                     for (int w = 0; w < 2; ++w)
 #pragma unroll
@@ -393,49 +450,51 @@ attn_decode_q4_kernel(const DecodeQ4Params p)
                                 mma_f16(acc[nt], a & LO, c & LO, a & HI, c & HI, bq[nt][q][2 * w + h][0],
                                         bq[nt][q][2 * w + h][1]);
                         }
-                    const float s0 = word_step(wl >> (16 * q)), s1 = word_step(wh >> (16 * q));
-                    const float z0 = word_zero(wl >> (16 * q)), z1 = word_zero(wh >> (16 * q));
+                    const float s0 = word_step(wl, q), s1 = word_step(wh, q);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
-                            const float v = fmaf(c < 2 ? -z0 : -z1, sq[nt][c & 1][q], acc[nt][c]);
                             const float s = c < 2 ? s0 : s1;
-                            x[tile][nt][c] = q == 0 ? v * s : fmaf(v, s, x[tile][nt][c]);
+                            x[tile][nt][c] = q == 0 ? acc[nt][c] * s : fmaf(acc[nt][c], s, x[tile][nt][c]);
                         }
                 }
+            }
+            if (biased) {                                // to the log2 domain, less slope |position - slot|
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) x[tile][nt][c] *= fac[nt][c & 1];
-            }
-            if (biased) {
+                    for (int c = 0; c < 2; ++c) {
+                        const RowInfo ri = info[8 * nt + 2 * t + c];
 #pragma unroll
-                for (int tile = 0; tile < 4; ++tile)
+                        for (int tile = 0; tile < 4; ++tile)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const int key = key0 + 16 * tile + pi + 8 * (c >> 1);
-                            x[tile][nt][c] = fmaf(-slope[nt][c & 1], fabsf(static_cast<float>(pos[nt][c & 1] - key)),
-                                                  x[tile][nt][c]);
-                        }
+                            for (int h = 0; h < 2; ++h) {
+                                const float away = fabsf(static_cast<float>(ri.pos - (key0 + 16 * tile + 8 * h + pi)));
+                                x[tile][nt][c + 2 * h] = fmaf(-ri.slope, away, x[tile][nt][c + 2 * h] * ri.fac);
+                            }
+                    }
             }
             if (masked) {
 #pragma unroll
-                for (int tile = 0; tile < 4; ++tile)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int c = 0; c < 2; ++c) {
+                        const int left = info[8 * nt + 2 * t + c].lim - key0 - pi;
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            if (key0 + 16 * tile + pi + 8 * (c >> 1) >= lim[nt][c & 1]) x[tile][nt][c] = -INFINITY;
+                        for (int tile = 0; tile < 4; ++tile)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                if (16 * tile + 8 * h >= left) x[tile][nt][c + 2 * h] = -INFINITY;
+                    }
             }
 
             // online softmax: x becomes the weights
             bool grew = false;
             float alpha[NT][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt) {
+                float m_use[2];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     float mx = fmaxf(x[0][nt][c], x[0][nt][c + 2]);
@@ -444,69 +503,101 @@ attn_decode_q4_kernel(const DecodeQ4Params p)
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                    const float m_new = fmaxf(m_run[nt][c], mx);
-                    const float m_use = m_new == -INFINITY ? 0.f : m_new;
-                    alpha[nt][c] = ex2_approx(m_run[nt][c] - m_use);
+                    const float m_new = fmaxf(m_run[nt][c], mx * ef[nt][c]);
+                    m_use[c] = m_new == -INFINITY ? 0.f : m_new;
+                    alpha[nt][c] = ex2_approx(m_run[nt][c] - m_use[c]);
                     grew = grew || m_new > m_run[nt][c];
-                    float sum = 0.f;
-#pragma unroll
-                    for (int tile = 0; tile < 4; ++tile) {
-                        x[tile][nt][c] = ex2_approx(x[tile][nt][c] - m_use);
-                        x[tile][nt][c + 2] = ex2_approx(x[tile][nt][c + 2] - m_use);
-                        sum += x[tile][nt][c] + x[tile][nt][c + 2];
-                    }
-                    l_run[nt][c] = fmaf(l_run[nt][c], alpha[nt][c], sum);
                     m_run[nt][c] = m_new;
                 }
+                const uint64_t e2 = f2_pack(ef[nt][0], ef[nt][1]), m2 = f2_pack(-m_use[0], -m_use[1]);
+                uint64_t sum = f2_pack(l_run[nt][0] * alpha[nt][0], l_run[nt][1] * alpha[nt][1]);
+#pragma unroll
+                for (int tile = 0; tile < 4; ++tile)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float a, c;
+                        f2_unpack(f2_fma(f2_pack(x[tile][nt][2 * h], x[tile][nt][2 * h + 1]), e2, m2), a, c);
+                        x[tile][nt][2 * h] = ex2_approx(a);
+                        x[tile][nt][2 * h + 1] = ex2_approx(c);
+                        sum = f2_add(sum, f2_pack(x[tile][nt][2 * h], x[tile][nt][2 * h + 1]));
+                    }
+                f2_unpack(sum, l_run[nt][0], l_run[nt][1]);
+            }
             if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int q = 0; q < NGV; ++q) {
-                        corr[nt][0][q] *= alpha[nt][0];
-                        corr[nt][1][q] *= alpha[nt][1];
+                    for (int c = 0; c < 4; ++c) {
+                        zc[nt][c] *= alpha[nt][c & 1];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
+                        for (int q = 0; q < NGV; ++q)
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) o[nt][q][j][c] *= alpha[nt][c & 1];
+                            for (int j = 0; j < 4; ++j) o[nt][q][j][c] *= alpha[nt][c & 1];
                     }
             }
 
-            // the value groups' steps, and the power of two that keeps p s R inside fp16
-            uint32_t vw[4][2];
-            float smax[NGV];
-#pragma unroll
-            for (int q = 0; q < NGV; ++q) smax[q] = 0.f;
+            // the value groups' words; R follows the largest step
+            uint32_t vw[4][2], top = 0u;
 #pragma unroll
             for (int tile = 0; tile < 4; ++tile)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const uint8_t* wb = sb + q4::v_words_off(DK, DV) + (16 * tile + 8 * h) * 2 * NGV + vw_lo;
-                    uint32_t w = NGV == 2 ? *reinterpret_cast<const uint32_t*>(wb) : *reinterpret_cast<const uint16_t*>(wb);
-                    if (masked && key0 + 16 * tile + 8 * h + pi >= end) w = 0u;   // never written, perhaps
-                    vw[tile][h] = w;
-#pragma unroll
-                    for (int q = 0; q < NGV; ++q) smax[q] = fmaxf(smax[q], word_step(w >> (16 * q)));   // a NaN step is passed over
+                    const uint8_t* wb = sb + vw_0 + (16 * tile + 8 * h) * 2 * NGV;
+                    vw[tile][h] = NGV == 2 ? *reinterpret_cast<const uint32_t*>(wb) : *reinterpret_cast<const uint16_t*>(wb);
                 }
-            bool over = false;
+            if (masked) {                                // slots that no row sees may hold anything
 #pragma unroll
-            for (int q = 0; q < NGV; ++q) over = over || rg[q] == 0.f || smax[q] * rg[q] > 32768.f;
-            if (__any_sync(0xffffffffu, over)) {
+                for (int tile = 0; tile < 4; ++tile)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (key0 + 16 * tile + 8 * h + pi >= end) vw[tile][h] = 0u;
+            }
+#pragma unroll
+            for (int tile = 0; tile < 4; ++tile) top = max_u16x2(top, max_u16x2(vw[tile][0], vw[tile][1]));
+            if (__any_sync(0xffffffffu, max_u16x2(top, thr) != thr)) {
 #pragma unroll
                 for (int q = 0; q < NGV; ++q) {
-                    const float top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(smax[q])));
-                    if (rg[q] != 0.f && top * rg[q] <= 32768.f) continue;
-                    const float r_new = pow2i(max(-126, min(126, 12 - exponent(top))));
-                    const float f = rg[q] == 0.f ? 0.f : r_new / rg[q];
-                    rg[q] = r_new;
+                    // the largest step (0x7F80 and up, a bad group, set aside), and the rows that a bad group reaches
+                    uint32_t big = 0u, poison = 0u;
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        corr[nt][0][q] *= f;
-                        corr[nt][1][q] *= f;
+                    for (int tile = 0; tile < 4; ++tile)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t w = (vw[tile][h] >> (16 * q)) & 0xFFFFu;
+                            if (w < 0x7F80u) {
+                                big = max(big, w);
+                            } else {
+                                vw[tile][h] &= q ? 0x0000FFFFu : 0xFFFF0000u;
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) o[nt][q][j][c] *= f;
+                                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                    for (int c = 0; c < 2; ++c)
+                                        if (x[tile][nt][c + 2 * h] != 0.f) poison |= 1u << (2 * nt + c);
+                            }
+                        }
+                    big = __reduce_max_sync(0xffffffffu, big);
+#pragma unroll
+                    for (int sh = 4; sh < 32; sh <<= 1) poison |= __shfl_xor_sync(0xffffffffu, poison, sh);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            if (poison >> (2 * nt + c) & 1u) zc[nt][2 * q + c] = __uint_as_float(0x7FC00000u);
+                    if (big > ((thr >> (16 * q)) & 0xFFFFu)) {
+                        const int ex = static_cast<int>(big >> 7) - 127;       // the largest s is in [2^ex, 2^(ex + 1))
+                        const float r_new = pow2i(min(126, 12 - ex));
+                        const float f = r_new / rg[q];
+                        rg[q] = r_new;
+                        thr = (thr & (q ? 0x0000FFFFu : 0xFFFF0000u)) | static_cast<uint32_t>((min(ex + 2 + 127, 254) << 7) | 0x7F) << (16 * q);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            zc[nt][2 * q] *= f;
+                            zc[nt][2 * q + 1] *= f;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                                for (int c = 0; c < 4; ++c) o[nt][q][j][c] *= f;
+                        }
                     }
                 }
             }
@@ -514,39 +605,36 @@ attn_decode_q4_kernel(const DecodeQ4Params p)
             // O^T += V^T (p s R)^T
 #pragma unroll
             for (int tile = 0; tile < 4; ++tile) {
-                uint32_t bp[NT][NGV][2];
-#pragma unroll
-                for (int q = 0; q < NGV; ++q) {
-                    const float s0 = word_step(vw[tile][0] >> (16 * q)) * rg[q], s1 = word_step(vw[tile][1] >> (16 * q)) * rg[q];
-                    const float z0 = word_zero(vw[tile][0] >> (16 * q)), z1 = word_zero(vw[tile][1] >> (16 * q));
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        float w[4];
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            w[c] = x[tile][nt][c] * (c < 2 ? s0 : s1);
-                            // a masked weight is 0 whatever the group's step (0 times NaN otherwise)
-                            if (masked && x[tile][nt][c] == 0.f) w[c] = 0.f;
-                            corr[nt][c & 1][q] = fmaf(w[c], c < 2 ? z0 : z1, corr[nt][c & 1][q]);
-                        }
-                        bp[nt][q][0] = transpose8(pack_f16x2(w[0], w[1]));
-                        bp[nt][q][1] = transpose8(pack_f16x2(w[2], w[3]));
-                    }
-                }
-                uint32_t vc[4][NGV];                     // slots t, t + 4, t + 8, t + 12 of the tile
+                uint32_t vc[4][NGV], vz[4];              // codes and words of slots t, t + 4, t + 8, t + 12 of the tile
                 const uint8_t* vb = sb + v_0 + tile * 16 * (DV / 2);
+                const uint8_t* zb = sb + vz_0 + tile * 16 * 2 * NGV;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     if (NGV == 2) {
                         const uint2 a = *reinterpret_cast<const uint2*>(vb + 4 * i * (DV / 2));
                         vc[i][0] = a.x;
                         vc[i][NGV - 1] = a.y;
+                        vz[i] = *reinterpret_cast<const uint32_t*>(zb + 4 * i * 2 * NGV);
                     } else {
                         vc[i][0] = *reinterpret_cast<const uint32_t*>(vb + 4 * i * (DV / 2));
+                        vz[i] = *reinterpret_cast<const uint16_t*>(zb + 4 * i * 2 * NGV);
                     }
                 }
 #pragma unroll
-                for (int q = 0; q < NGV; ++q)
+                for (int q = 0; q < NGV; ++q) {
+                    const float s0 = word_step(vw[tile][0], q) * rg[q], s1 = word_step(vw[tile][1], q) * rg[q];
+                    uint32_t bp[NT][2];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        bp[nt][0] = transpose8(pack_f16x2(x[tile][nt][0] * s0, x[tile][nt][1] * s0));
+                        bp[nt][1] = transpose8(pack_f16x2(x[tile][nt][2] * s1, x[tile][nt][3] * s1));
+                    }
+                    // the zeros: group 0's in the accumulator's rows 0-7, group 1's in 8-15
+                    const uint32_t z0 = __byte_perm(vz[0], vz[1], q ? 0x7632 : 0x5410) & LO;
+                    const uint32_t z1 = __byte_perm(vz[2], vz[3], q ? 0x7632 : 0x5410) & LO;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma_f16(zc[nt], q ? 0u : z0, q ? z0 : 0u, q ? 0u : z1, q ? z1 : 0u, bp[nt][0], bp[nt][1]);
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf) {     // codes 4 hf .. 4 hf + 3 of both slots of a pair
                         const uint32_t a = __byte_perm(vc[0][q], vc[1][q], hf ? 0x7632 : 0x5410);
@@ -556,35 +644,21 @@ attn_decode_q4_kernel(const DecodeQ4Params p)
                             const uint32_t as = a >> (8 * jj), cs = c >> (8 * jj);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
-                                mma_f16(o[nt][q][2 * hf + jj], as & LO, as & HI, cs & LO, cs & HI, bp[nt][q][0], bp[nt][q][1]);
+                                mma_f16(o[nt][q][2 * hf + jj], as & LO, as & HI, cs & LO, cs & HI, bp[nt][0], bp[nt][1]);
                         }
                     }
+                }
             }
             ++landed;
             __syncwarp();                                // every lane is done with the stage
-            if (it + L::STAGES < count) {
-                // (issue() counts from the first block that has not landed)
-                if (lane == 0) {
-                    const uint32_t s = stage;
-                    mbar_arrive_expect_tx(bar0 + 8u * s, L::BYTES_BLOCK);
-                    bulk_load(sbase + (warp * L::STAGES + s) * L::BYTES_BLOCK,
-                              src + static_cast<int64_t>(warp + WARPS * (it + L::STAGES)) * L::BYTES_BLOCK, L::BYTES_BLOCK,
-                              bar0 + 8u * s);
-                }
-                ++issued;
-            }
+            if (ahead.todo > 0) issue();
         }
-        if (!ok) {
-            // land what is still in flight before the ring is written or the CTA ends
-            const uint64_t t0 = globaltimer_ns();
-            for (uint32_t i = landed % L::STAGES, k = 0; issued > 0 && k < L::STAGES; ++k, i = (i + 1) % L::STAGES)
-                while (!mbar_test(bar0 + 8u * i, ((landed + k) / L::STAGES) & 1u) && globaltimer_ns() - t0 < 100000000ull) {
-                }
-        }
+        if (!ok) break;
 
-        // -------------------------------------------- merge the four warps (the ring is free now)
-        __syncthreads();
-        float* red = reinterpret_cast<float*>(smem) + warp * L::RED_WARP;
+        // -------------------------------------------- write the pair, or this warp's part of it
+        const bool ends = last == nb;
+        const bool whole = ends && !mid_pair;
+        const int64_t part0 = static_cast<int64_t>(2 * worker + (mid_pair ? 0 : 1)) * p.part_rows;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -593,121 +667,143 @@ attn_decode_q4_kernel(const DecodeQ4Params p)
                 float l = l_run[nt][c];
 #pragma unroll
                 for (int sh = 4; sh < 32; sh <<= 1) l += __shfl_xor_sync(0xffffffffu, l, sh);
-                if (g == 0) {
-                    red[row] = m_run[nt][c];
-                    red[L::ROWS + row] = l;
-                }
+                if (row >= rows) continue;
+                const float m_use = m_run[nt][c] == -INFINITY ? 0.f : m_run[nt][c];
+                const int64_t orow = pair_bh * p.R + r0 + row;
+                // (a NaN sum is not 0: it reaches the output)
+                const float inv_l = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
 #pragma unroll
                 for (int q = 0; q < NGV; ++q) {
-                    float z = corr[nt][c][q];
-#pragma unroll
-                    for (int sh = 4; sh < 32; sh <<= 1) z += __shfl_xor_sync(0xffffffffu, z, sh);
-                    const float inv = rg[q] == 0.f ? 0.f : 1.f / rg[q];
-                    float* dst = red + 2 * L::ROWS + row * DV + 64 * q + 8 * g;
+                    const float f = inv_l / rg[q];
+                    float v[8];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        dst[2 * j] = fmaf(o[nt][q][j][c], TWO24, -z) * inv;
-                        dst[2 * j + 1] = fmaf(o[nt][q][j][c + 2], TWO20, -z) * inv;
+                        // (u0 2^-24 as the even channels' u)
+                        v[2 * j] = (o[nt][q][j][c] - zc[nt][2 * q + c]) * TWO24 * f;
+                        v[2 * j + 1] = fmaf(o[nt][q][j][c + 2], TWO20, -zc[nt][2 * q + c] * TWO24) * f;
+                    }
+                    if (whole) {
+                        uint4 w;
+                        w.x = pack_bf16x2(v[0], v[1]);
+                        w.y = pack_bf16x2(v[2], v[3]);
+                        w.z = pack_bf16x2(v[4], v[5]);
+                        w.w = pack_bf16x2(v[6], v[7]);
+                        *reinterpret_cast<uint4*>(p.O + orow * DV + 64 * q + 8 * g) = w;
+                    } else {
+                        float4* dst = reinterpret_cast<float4*>(p.part_o + (part0 + row) * DV + 64 * q + 8 * g);
+                        dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+                        dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+                    }
+                }
+                if (g == 0) {
+                    if (!whole) {
+                        *reinterpret_cast<float2*>(p.part_ml + 2 * (part0 + row)) = make_float2(m_run[nt][c], l);
+                    } else if (p.LSE != nullptr) {
+                        p.LSE[orow] = l == 0.f ? -INFINITY : (m_use + __log2f(l)) * LN2;
                     }
                 }
             }
-        __syncthreads();
-        const bool ends = blk + take == nb;
-        const bool whole = ends && !mid_pair;
-        const int part = 2 * cta + (mid_pair ? 0 : 1);
-        const int rows = min(L::ROWS, p.R - r0);
-        const float* all = reinterpret_cast<const float*>(smem);
-        for (int e = threadIdx.x; e < rows * DV; e += THREADS) {
-            const int row = e / DV, c = e % DV;
-            float M = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < WARPS; ++w) M = fmaxf(M, all[w * L::RED_WARP + row]);
-            const float M_use = M == -INFINITY ? 0.f : M;
-            float Lsum = 0.f, Oc = 0.f;
-#pragma unroll
-            for (int w = 0; w < WARPS; ++w) {
-                const float* rw = all + w * L::RED_WARP;
-                const float f = ex2_approx(rw[row] - M_use);
-                Lsum = fmaf(rw[L::ROWS + row], f, Lsum);
-                Oc = fmaf(rw[2 * L::ROWS + row * DV + c], f, Oc);
-            }
-            if (whole) {
-                const int64_t orow = pair_bh * p.R + r0 + row;
-                // (a NaN sum is not 0: it reaches the output)
-                const float out = Lsum == 0.f ? 0.f : Oc / Lsum;
-                p.O[orow * DV + c] = static_cast<uint16_t>(pack_bf16x2(out, 0.f) & 0xFFFFu);
-                if (c == 0 && p.LSE != nullptr) p.LSE[orow] = Lsum == 0.f ? -INFINITY : (M_use + __log2f(Lsum)) * LN2;
-            } else {
-                const int64_t prow = static_cast<int64_t>(part) * p.part_rows + row;
-                p.part_o[prow * DV + c] = Oc;
-                if (c == 0) {
-                    p.part_ml[2 * prow] = M;
-                    p.part_ml[2 * prow + 1] = Lsum;
-                }
-            }
-        }
-        if (!whole) {
-            if (mid_pair) head_end = ends ? 1 : 0;
-            else tail_pair = static_cast<int>(pair_bh) * p.row_tiles + rt;
-        }
-        fence_proxy_async_smem();                        // the merge's writes come before the next copies into the ring
-        __syncthreads();
-
-        todo -= take;
-        blk = 0;
-        mid_pair = false;
-        if (++pr == pairs_b) {
-            pr = 0;
-            ++b;
+        if (p.split && lane == 0 && !mid_pair) p.pair_first[pair] = whole ? -1 : worker;
+        if (mid_pair && ends) head_end = 1;
+        at.todo -= p.split ? last - at.blk : 1;
+        at.blk = 0;
+        if (++at.pr == pairs_b) {
+            at.pr = 0;
+            ++at.b;
+            if (at.todo > 0) at.nb = pair_blocks(p, at.b);
         }
     }
-    if (p.split && threadIdx.x == 0) p.part_flags[cta] = make_int2(tail_pair, head_end);
+    if (!ok) {
+        // land what is still in flight before the CTA's shared memory is given up
+        const uint64_t t0 = globaltimer_ns();
+        for (uint32_t i = landed; i < issued; ++i)
+            while (!mbar_test(bar0 + 8u * (i % L::STAGES), (i / L::STAGES) & 1u) && globaltimer_ns() - t0 < 100000000ull) {
+            }
+    }
+    if (p.split && lane == 0) p.part_ends[worker] = head_end;
 }
 
-// Merge of the parts of a cut pair: CTA (c, row) for the pair whose first part is
-// CTA c's slot 1; the parts after it are the slots 0 of CTAs c + 1, c + 2, ... up to the
-// one that ends the pair. One thread per output column.
+// Merge of the parts of the cut pairs: CTA (pair, two of its rows), four warps to a
+// row. The first part is slot 1 of worker pair_first[pair]; the parts after it are the
+// slots 0 of the workers that follow, up to the one that ends the pair.
 template <int DV>
-__global__ void __launch_bounds__(DV)
+__global__ void __launch_bounds__(256)
 attn_decode_q4_merge_kernel(const DecodeQ4Params p, int tile_rows)
 {
+    constexpr int CPL = DV / 32;
+    __shared__ float red[8][DV];
     griddep_wait();   // the parts are visible
-    const int c = static_cast<int>(blockIdx.x), row = static_cast<int>(blockIdx.y);
-    const int pair = p.part_flags[c].x;
-    if (pair < 0) return;
+    const int64_t pair = blockIdx.x;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, sub = warp % 4;
+    const int first = p.pair_first[pair];
+    if (first < 0 || first >= p.warps) return;           // whole
+    const int row = static_cast<int>(blockIdx.y) * 2 + warp / 4;
     const int64_t pair_bh = pair / p.row_tiles;
-    const int r = (pair % p.row_tiles) * tile_rows + row;
-    if (r >= p.R) return;
-    int parts = 1;                                       // one warp-wide look at the flags per 32 parts
-    for (int base = c + 1;; base += 32) {
-        const int i = base + static_cast<int>(threadIdx.x % 32);
-        const uint32_t ends = __ballot_sync(0xffffffffu, i >= p.ctas || p.part_flags[i].y != 0);
+    const int r = static_cast<int>(pair - pair_bh * p.row_tiles) * tile_rows + row;
+    const bool live = row < p.part_rows && r < p.R;
+    int parts = 1;                                       // one look at the flags per 32 parts
+    for (int base = first + 1;; base += 32) {
+        const int i = base + lane;
+        const uint32_t ends = __ballot_sync(0xffffffffu, i >= p.warps || p.part_ends[i] != 0);
         if (ends != 0u) {
             parts += __ffs(ends);
             break;
         }
         parts += 32;
     }
-    parts = min(parts, p.ctas - c);
+    parts = min(parts, p.warps - first);
     auto part_row = [&](int s) -> int64_t {
-        return static_cast<int64_t>(s == 0 ? 2 * c + 1 : 2 * (c + s)) * p.part_rows + row;
+        return static_cast<int64_t>(s == 0 ? 2 * first + 1 : 2 * (first + s)) * p.part_rows + row;
     };
-    float M = -INFINITY;
+    float M = -INFINITY, Lsum = 0.f, acc[CPL];
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) acc[c] = 0.f;
+    if (live) {
+        for (int s = lane; s < parts; s += 32) M = fmaxf(M, p.part_ml[2 * part_row(s)]);
+#pragma unroll
+        for (int sh = 16; sh > 0; sh >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, sh));
+        const float M_use = M == -INFINITY ? 0.f : M;
+        for (int s = lane; s < parts; s += 32) {
+            const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * part_row(s));
+            Lsum = fmaf(ml.y, ex2_approx(ml.x - M_use), Lsum);
+        }
+#pragma unroll
+        for (int sh = 16; sh > 0; sh >>= 1) Lsum += __shfl_xor_sync(0xffffffffu, Lsum, sh);
 #pragma unroll 4
-    for (int s = 0; s < parts; ++s) M = fmaxf(M, p.part_ml[2 * part_row(s)]);
-    const float M_use = M == -INFINITY ? 0.f : M;
-    float Lsum = 0.f, Oc = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < parts; ++s) {
-        const int64_t pr = part_row(s);
-        const float f = ex2_approx(p.part_ml[2 * pr] - M_use);
-        Lsum = fmaf(p.part_ml[2 * pr + 1], f, Lsum);
-        Oc = fmaf(p.part_o[pr * DV + threadIdx.x], f, Oc);
+        for (int s = sub; s < parts; s += 4) {
+            const int64_t pr = part_row(s);
+            const float f = ex2_approx(p.part_ml[2 * pr] - M_use);
+            if (CPL == 4) {
+                const float4 v = *reinterpret_cast<const float4*>(p.part_o + pr * DV + 4 * lane);
+                acc[0] = fmaf(v.x, f, acc[0]);
+                acc[1] = fmaf(v.y, f, acc[1]);
+                acc[CPL - 2] = fmaf(v.z, f, acc[CPL - 2]);
+                acc[CPL - 1] = fmaf(v.w, f, acc[CPL - 1]);
+            } else {
+                const float2 v = *reinterpret_cast<const float2*>(p.part_o + pr * DV + 2 * lane);
+                acc[0] = fmaf(v.x, f, acc[0]);
+                acc[1] = fmaf(v.y, f, acc[1]);
+            }
+        }
+        M = M_use;
     }
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) red[warp][CPL * lane + c] = acc[c];
+    __syncthreads();
+    if (sub != 0 || !live) return;
     const int64_t orow = pair_bh * p.R + r;
-    const float out = Lsum == 0.f ? 0.f : Oc / Lsum;
-    p.O[orow * DV + threadIdx.x] = static_cast<uint16_t>(pack_bf16x2(out, 0.f) & 0xFFFFu);
-    if (threadIdx.x == 0 && p.LSE != nullptr) p.LSE[orow] = Lsum == 0.f ? -INFINITY : (M_use + __log2f(Lsum)) * LN2;
+    const float inv = Lsum == 0.f ? 0.f : 1.f / Lsum;
+#pragma unroll
+    for (int c = 0; c < CPL; c += 2) {
+        float v[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int d = CPL * lane + c + h;
+            v[h] = (red[warp][d] + red[warp + 1][d] + red[warp + 2][d] + red[warp + 3][d]) * inv;
+        }
+        *reinterpret_cast<uint32_t*>(p.O + orow * DV + CPL * lane + c) = pack_bf16x2(v[0], v[1]);
+    }
+    if (lane == 0 && p.LSE != nullptr) p.LSE[orow] = Lsum == 0.f ? -INFINITY : (M + __log2f(Lsum)) * LN2;
 }
 
 template <int DK, int DV, int NT>
@@ -725,10 +821,12 @@ cudaError_t launch(const DecodeQ4Params& p, cudaStream_t stream)
         if (e != cudaSuccess) return e;
         configured[dev] = true;
     }
-    e = launch_pdl(kern, dim3(static_cast<unsigned>(p.ctas)), dim3(THREADS), L::BYTES, stream, p);
+    const unsigned ctas = static_cast<unsigned>((p.warps + WARPS - 1) / WARPS);
+    e = launch_pdl(kern, dim3(ctas), dim3(THREADS), L::BYTES, stream, p);
     if (e != cudaSuccess || !p.split) return e;
-    return launch_pdl(attn_decode_q4_merge_kernel<DV>, dim3(static_cast<unsigned>(p.ctas), static_cast<unsigned>(p.part_rows)),
-                      dim3(DV), 0, stream, p, L::ROWS);
+    const unsigned pairs = static_cast<unsigned>(static_cast<int64_t>(p.B) * p.H_kv * p.row_tiles);
+    return launch_pdl(attn_decode_q4_merge_kernel<DV>, dim3(pairs, static_cast<unsigned>((p.part_rows + 1) / 2)), dim3(256), 0,
+                      stream, p, L::ROWS);
 }
 
 }  // namespace dq4
