@@ -1135,7 +1135,7 @@ extern "C" int attn_decode_q4(const void* Q, const void* cache, int B, int H, in
     const Q4Plan w = q4_plan(B, H, H_kv, n, m, d_k, d_v);
     if (w.total > 0 && (workspace == nullptr || workspace_bytes < w.total)) return ATTN_ERR_INVALID_ARG;
     if (w.total > 0 && !aligned(workspace, kWsAlign)) return ATTN_ERR_MISALIGNED;
-    if (w.few && w.pairs > INT32_MAX) return ATTN_ERR_UNSUPPORTED;
+    if (w.few && w.pairs * q4_blocks(m) > INT32_MAX) return ATTN_ERR_UNSUPPORTED;
     uint32_t* status = nullptr;
     if ((rc = status_word(&status)) != ATTN_OK) return rc;
     uint8_t* wsb = static_cast<uint8_t*>(workspace);

@@ -171,66 +171,75 @@ struct Cursor {
     }
 };
 
-// Warp w's share of the sequence.
+// Worker w's share of the sequence (idle workers, where there are fewer units than
+// workers, come last).
 __device__ __forceinline__ Cursor first_block(const DecodeQ4Params& p, int w, int lane, int pairs_b)
 {
     Cursor c;
-    if (!p.split) {
-        const int64_t pairs = static_cast<int64_t>(p.B) * pairs_b;
-        const int64_t p0 = pairs * w / p.warps;
-        c.todo = static_cast<int>(pairs * (w + 1) / p.warps - p0);
-        c.b = static_cast<int>(p0 / pairs_b);
-        c.pr = static_cast<int>(p0 - static_cast<int64_t>(c.b) * pairs_b);
-        c.blk = 0;
-        c.nb = c.todo > 0 ? pair_blocks(p, c.b) : 1;
-        return c;
-    }
-    const bool ragged = mask_has_lengths(p.mask);
-    int64_t total;
-    if (ragged) {
-        int64_t sum = 0;
-        for (int i = lane; i < p.B; i += 32) sum += pair_blocks(p, i);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        total = sum * pairs_b;
-    } else {
-        total = static_cast<int64_t>(p.B) * pairs_b * pair_blocks(p, 0);
-    }
-    const int64_t warps = min(static_cast<int64_t>(p.warps), total);
-    const int64_t u0 = total * min(static_cast<int64_t>(w), warps) / warps;
-    const int64_t u1 = total * min(static_cast<int64_t>(w) + 1, warps) / warps;
-    c.todo = static_cast<int>(u1 - u0);
     c.b = c.pr = c.blk = 0;
     c.nb = 1;
-    if (c.todo == 0) return c;
-    int64_t before = 0;                                  // units of the entries before b
+    constexpr int HELD = 4;                              // entries per lane that are looked at once
+    int nb[HELD];
+    const bool ragged = p.split && mask_has_lengths(p.mask);
+    uint32_t total;
     if (ragged) {
-        for (int base = 0; base < p.B; base += 32) {
-            const int64_t nb = base + lane < p.B ? static_cast<int64_t>(pair_blocks(p, base + lane)) * pairs_b : 0;
-            int64_t incl = nb;
+        uint32_t sum = 0;
+#pragma unroll
+        for (int k = 0; k < HELD; ++k) {
+            const int i = 32 * k + lane;
+            nb[k] = i < p.B ? pair_blocks(p, i) * pairs_b : 0;
+            sum += nb[k];
+        }
+        for (int i = 32 * HELD + lane; i < p.B; i += 32) sum += pair_blocks(p, i) * pairs_b;
+        total = __reduce_add_sync(0xffffffffu, sum);
+    } else {
+        total = static_cast<uint32_t>(p.B) * pairs_b * (p.split ? pair_blocks(p, 0) : 1);
+    }
+    const uint32_t each = total / p.warps, more = total - each * p.warps;
+    uint32_t u0 = each * w + min(static_cast<uint32_t>(w), more);
+    c.todo = static_cast<int>(each + (static_cast<uint32_t>(w) < more ? 1u : 0u));
+    if (c.todo == 0) return c;
+    if (!p.split) {
+        c.b = static_cast<int>(u0 / pairs_b);
+        c.pr = static_cast<int>(u0 - static_cast<uint32_t>(c.b) * pairs_b);
+        c.nb = pair_blocks(p, c.b);
+        return c;
+    }
+    if (ragged) {
+        int units = 0;
+        uint32_t before = 0;                             // units of the entries before the 32 looked at
+        for (int base = 0;; base += 32) {
+            units = 0;
+            if (base < 32 * HELD) {
+#pragma unroll
+                for (int k = 0; k < HELD; ++k) units = base == 32 * k ? nb[k] : units;
+            } else if (base + lane < p.B) {
+                units = pair_blocks(p, base + lane) * pairs_b;
+            }
+            uint32_t incl = units;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
-                const int64_t v = __shfl_up_sync(0xffffffffu, incl, off);
+                const uint32_t v = __shfl_up_sync(0xffffffffu, incl, off);
                 if (lane >= off) incl += v;
             }
             const uint32_t past = __ballot_sync(0xffffffffu, before + incl > u0);
             if (past != 0u) {
                 const int l = __ffs(past) - 1;
                 c.b = base + l;
-                before += __shfl_sync(0xffffffffu, incl - nb, l);
+                u0 -= before + __shfl_sync(0xffffffffu, incl - units, l);
+                c.nb = __shfl_sync(0xffffffffu, units, l) / pairs_b;
                 break;
             }
             before += __shfl_sync(0xffffffffu, incl, 31);
         }
-        c.nb = pair_blocks(p, c.b);
     } else {
         c.nb = pair_blocks(p, 0);
-        const int64_t per = static_cast<int64_t>(pairs_b) * c.nb;
+        const uint32_t per = static_cast<uint32_t>(pairs_b) * c.nb;
         c.b = static_cast<int>(u0 / per);
-        before = per * c.b;
+        u0 -= per * c.b;
     }
-    c.pr = static_cast<int>((u0 - before) / c.nb);
-    c.blk = static_cast<int>((u0 - before) - static_cast<int64_t>(c.pr) * c.nb);
+    c.pr = static_cast<int>(u0) / c.nb;
+    c.blk = static_cast<int>(u0) - c.pr * c.nb;
     return c;
 }
 
@@ -723,87 +732,86 @@ attn_decode_q4_kernel(const DecodeQ4Params p)
     if (p.split && lane == 0) p.part_ends[worker] = head_end;
 }
 
-// Merge of the parts of the cut pairs: CTA (pair, two of its rows), four warps to a
-// row. The first part is slot 1 of worker pair_first[pair]; the parts after it are the
+// Merge of the parts of the cut pairs: CTA (pair, row), the parts dealt out to its
+// warps. The first part is slot 1 of worker pair_first[pair]; the parts after it are the
 // slots 0 of the workers that follow, up to the one that ends the pair.
+constexpr int MERGE_WARPS = 8;
+
 template <int DV>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(32 * MERGE_WARPS)
 attn_decode_q4_merge_kernel(const DecodeQ4Params p, int tile_rows)
 {
     constexpr int CPL = DV / 32;
-    __shared__ float red[8][DV];
+    __shared__ float red[MERGE_WARPS][DV];
     griddep_wait();   // the parts are visible
     const int64_t pair = blockIdx.x;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, sub = warp % 4;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int first = p.pair_first[pair];
     if (first < 0 || first >= p.warps) return;           // whole
-    const int row = static_cast<int>(blockIdx.y) * 2 + warp / 4;
+    const int row = static_cast<int>(blockIdx.y);
     const int64_t pair_bh = pair / p.row_tiles;
     const int r = static_cast<int>(pair - pair_bh * p.row_tiles) * tile_rows + row;
-    const bool live = row < p.part_rows && r < p.R;
-    int parts = 1;                                       // one look at the flags per 32 parts
-    for (int base = first + 1;; base += 32) {
-        const int i = base + lane;
-        const uint32_t ends = __ballot_sync(0xffffffffu, i >= p.warps || p.part_ends[i] != 0);
-        if (ends != 0u) {
-            parts += __ffs(ends);
-            break;
-        }
-        parts += 32;
-    }
-    parts = min(parts, p.warps - first);
+    if (r >= p.R) return;
+    // worker first + s has part s; lane l looks at parts l, l + 32, ... until one ends the pair
     auto part_row = [&](int s) -> int64_t {
         return static_cast<int64_t>(s == 0 ? 2 * first + 1 : 2 * (first + s)) * p.part_rows + row;
     };
-    float M = -INFINITY, Lsum = 0.f, acc[CPL];
+    int parts = 0;
+    float M = -INFINITY, Lsum = 0.f;
+    for (int base = 0;; base += 32) {
+        const int s = base + lane;
+        const bool there = first + s < p.warps;
+        const float2 ml = there ? *reinterpret_cast<const float2*>(p.part_ml + 2 * part_row(s)) : make_float2(-INFINITY, 0.f);
+        const uint32_t ends = __ballot_sync(0xffffffffu, !there || (s > 0 && p.part_ends[first + s] != 0));
+        const int n = ends != 0u ? __ffs(ends) : 32;     // parts of these 32
+        float m = lane < n ? ml.x : -INFINITY, l = lane < n ? ml.y : 0.f;
+        const float mine = m;
+#pragma unroll
+        for (int sh = 16; sh > 0; sh >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, sh));
+        const float m_new = fmaxf(M, m), m_use = m_new == -INFINITY ? 0.f : m_new;
+        l = lane < n ? l * ex2_approx(mine - m_use) : 0.f;
+#pragma unroll
+        for (int sh = 16; sh > 0; sh >>= 1) l += __shfl_xor_sync(0xffffffffu, l, sh);
+        Lsum = fmaf(Lsum, ex2_approx(M - m_use), l);
+        M = m_new;
+        parts += n;
+        if (ends != 0u) break;
+    }
+    parts = min(parts, p.warps - first);
+    const float M_use = M == -INFINITY ? 0.f : M;
+    float acc[CPL];
 #pragma unroll
     for (int c = 0; c < CPL; ++c) acc[c] = 0.f;
-    if (live) {
-        for (int s = lane; s < parts; s += 32) M = fmaxf(M, p.part_ml[2 * part_row(s)]);
-#pragma unroll
-        for (int sh = 16; sh > 0; sh >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, sh));
-        const float M_use = M == -INFINITY ? 0.f : M;
-        for (int s = lane; s < parts; s += 32) {
-            const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * part_row(s));
-            Lsum = fmaf(ml.y, ex2_approx(ml.x - M_use), Lsum);
+#pragma unroll 8
+    for (int s = warp; s < parts; s += MERGE_WARPS) {
+        const int64_t pr = part_row(s);
+        const float f = ex2_approx(p.part_ml[2 * pr] - M_use);
+        if (CPL == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(p.part_o + pr * DV + 4 * lane);
+            acc[0] = fmaf(v.x, f, acc[0]);
+            acc[1] = fmaf(v.y, f, acc[1]);
+            acc[CPL - 2] = fmaf(v.z, f, acc[CPL - 2]);
+            acc[CPL - 1] = fmaf(v.w, f, acc[CPL - 1]);
+        } else {
+            const float2 v = *reinterpret_cast<const float2*>(p.part_o + pr * DV + 2 * lane);
+            acc[0] = fmaf(v.x, f, acc[0]);
+            acc[1] = fmaf(v.y, f, acc[1]);
         }
-#pragma unroll
-        for (int sh = 16; sh > 0; sh >>= 1) Lsum += __shfl_xor_sync(0xffffffffu, Lsum, sh);
-#pragma unroll 4
-        for (int s = sub; s < parts; s += 4) {
-            const int64_t pr = part_row(s);
-            const float f = ex2_approx(p.part_ml[2 * pr] - M_use);
-            if (CPL == 4) {
-                const float4 v = *reinterpret_cast<const float4*>(p.part_o + pr * DV + 4 * lane);
-                acc[0] = fmaf(v.x, f, acc[0]);
-                acc[1] = fmaf(v.y, f, acc[1]);
-                acc[CPL - 2] = fmaf(v.z, f, acc[CPL - 2]);
-                acc[CPL - 1] = fmaf(v.w, f, acc[CPL - 1]);
-            } else {
-                const float2 v = *reinterpret_cast<const float2*>(p.part_o + pr * DV + 2 * lane);
-                acc[0] = fmaf(v.x, f, acc[0]);
-                acc[1] = fmaf(v.y, f, acc[1]);
-            }
-        }
-        M = M_use;
     }
 #pragma unroll
     for (int c = 0; c < CPL; ++c) red[warp][CPL * lane + c] = acc[c];
     __syncthreads();
-    if (sub != 0 || !live) return;
     const int64_t orow = pair_bh * p.R + r;
     const float inv = Lsum == 0.f ? 0.f : 1.f / Lsum;
+    if (threadIdx.x < DV / 2) {
+        float v[2] = {0.f, 0.f};
 #pragma unroll
-    for (int c = 0; c < CPL; c += 2) {
-        float v[2];
+        for (int w = 0; w < MERGE_WARPS; ++w)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int d = CPL * lane + c + h;
-            v[h] = (red[warp][d] + red[warp + 1][d] + red[warp + 2][d] + red[warp + 3][d]) * inv;
-        }
-        *reinterpret_cast<uint32_t*>(p.O + orow * DV + CPL * lane + c) = pack_bf16x2(v[0], v[1]);
+            for (int h = 0; h < 2; ++h) v[h] += red[w][2 * threadIdx.x + h];
+        *reinterpret_cast<uint32_t*>(p.O + orow * DV + 2 * threadIdx.x) = pack_bf16x2(v[0] * inv, v[1] * inv);
     }
-    if (lane == 0 && p.LSE != nullptr) p.LSE[orow] = Lsum == 0.f ? -INFINITY : (M + __log2f(Lsum)) * LN2;
+    if (threadIdx.x == 0 && p.LSE != nullptr) p.LSE[orow] = Lsum == 0.f ? -INFINITY : (M_use + __log2f(Lsum)) * LN2;
 }
 
 template <int DK, int DV, int NT>
@@ -825,8 +833,8 @@ cudaError_t launch(const DecodeQ4Params& p, cudaStream_t stream)
     e = launch_pdl(kern, dim3(ctas), dim3(THREADS), L::BYTES, stream, p);
     if (e != cudaSuccess || !p.split) return e;
     const unsigned pairs = static_cast<unsigned>(static_cast<int64_t>(p.B) * p.H_kv * p.row_tiles);
-    return launch_pdl(attn_decode_q4_merge_kernel<DV>, dim3(pairs, static_cast<unsigned>((p.part_rows + 1) / 2)), dim3(256), 0,
-                      stream, p, L::ROWS);
+    return launch_pdl(attn_decode_q4_merge_kernel<DV>, dim3(pairs, static_cast<unsigned>(p.part_rows)),
+                      dim3(32 * MERGE_WARPS), 0, stream, p, L::ROWS);
 }
 
 }  // namespace dq4
