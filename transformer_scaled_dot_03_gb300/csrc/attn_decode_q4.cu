@@ -6,7 +6,9 @@ namespace attn {
 template <int DK, int DV>
 static cudaError_t launch_rows(const DecodeQ4Params& p, cudaStream_t stream)
 {
-    return decode_q4_tile_rows(p.R) == 8 ? dq4::launch<DK, DV, 1>(p, stream) : dq4::launch<DK, DV, 2>(p, stream);
+    if (p.R > 8) return dq4::launch<DK, DV, 2, false>(p, stream);
+    if (DV == 128 && p.R <= 4) return dq4::launch<DK, DV, 1, DV == 128>(p, stream);
+    return dq4::launch<DK, DV, 1, false>(p, stream);
 }
 
 cudaError_t launch_decode_q4(int d_k, int d_v, const DecodeQ4Params& p, cudaStream_t stream)

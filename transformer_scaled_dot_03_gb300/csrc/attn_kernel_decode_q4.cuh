@@ -24,7 +24,13 @@
 //
 // The zeros are nibbles too, and both terms with u0 are one more product each: for the
 // scores A holds the u0 of a slot's groups and B -sum_c q_c (as the sum of two fp16), for
-// the output A holds the slots' u0 in every row.
+// the output A's even rows hold the slots' u0 of group 0 and its odd rows those of group 1.
+// For V the odd nibbles are not masked off: the byte 16 u' + u is a subnormal too, and the
+// odd channel's sum is the byte's less the even channel's, taken at the end.
+//
+// Up to four rows with two value groups (PACK): columns 0-3 of every accumulator are
+// the rows with the weights of group 0, columns 4-7 the same rows with those of group 1,
+// so that one set of weights (scaled, packed, transposed once) serves both groups.
 //
 // The scores' accumulator has a slot in its row and two query rows in its columns; the
 // weights go to the second product's B operand through movmatrix (an 8 x 8 transpose
@@ -62,9 +68,9 @@ constexpr float LOG2E = 1.44269504088896341f;
 constexpr uint32_t LO = 0x000F000Fu, HI = 0x00F000F0u;
 constexpr float TWO20 = 1048576.f, TWO24 = 16777216.f;
 
-template <int DK, int DV, int NT>
+template <int DK, int DV, int NT, bool PACK>
 struct Layout {
-    static constexpr int ROWS = 8 * NT;
+    static constexpr int ROWS = PACK ? 4 : 8 * NT;
     static constexpr int BYTES_BLOCK = q4::block_bytes(DK, DV);
     // 2 blocks of 8704 or 6528 bytes, or 3 of 4352, in flight per warp
     static constexpr int STAGES = DK + DV == 128 ? 3 : 2;
@@ -73,7 +79,7 @@ struct Layout {
     static constexpr int BAR_OFF = ROW_OFF + WARPS * ROWS * 16;
     static constexpr int MISC_OFF = BAR_OFF + (WARPS * STAGES + 1) * 8;
     static constexpr int BYTES = MISC_OFF + 16 + 128;
-    static_assert(BYTES * decode_q4_ctas_per_sm(DK, DV, ROWS) <= 232448 - 3 * 1024, "shared memory budget");
+    static_assert(BYTES * decode_q4_ctas_per_sm(DK, DV, 8 * NT) <= 232448 - 3 * 1024, "shared memory budget");
 };
 
 // What the masks and the distance bias need to know of a query row.
@@ -243,12 +249,14 @@ __device__ __forceinline__ Cursor first_block(const DecodeQ4Params& p, int w, in
     return c;
 }
 
-template <int DK, int DV, int NT>
+template <int DK, int DV, int NT, bool PACK>
 __global__ void __launch_bounds__(THREADS, decode_q4_ctas_per_sm(DK, DV, 8 * NT))
 attn_decode_q4_kernel(const DecodeQ4Params p)
 {
-    using L = Layout<DK, DV, NT>;
+    using L = Layout<DK, DV, NT, PACK>;
     constexpr int NGK = DK / q4::GROUP, NGV = DV / q4::GROUP;
+    constexpr int SETS = PACK ? 1 : NGV;                 // sets of weights
+    static_assert(!PACK || (NT == 1 && NGV == 2), "columns for two groups of four rows");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
     const uint32_t sbase = smem_u32(smem);
@@ -297,7 +305,8 @@ attn_decode_q4_kernel(const DecodeQ4Params p)
     const int k_lo = q4::k_row(pi, DK) * (DK / 2) + t * 8 * NGK, k_hi = q4::k_row(pi + 8, DK) * (DK / 2) + t * 8 * NGK;
     const int v_0 = q4::v_off(DK) + q4::v_code_off(t, 0, g, DV);
     const int kw_0 = q4::k_words_off(DK) + 2 * NGK * pi, vw_0 = q4::v_words_off(DK, DV) + 2 * NGV * pi;
-    const int vz_0 = q4::v_words_off(DK, DV) + 2 * NGV * t;
+    auto row_of = [](int column) { return PACK ? column & 3 : column; };
+    const int own_shift = PACK && t >= 2 ? 0 : 16;       // brings the step of set 0 in a word to the upper half
     const bool biased = p.slopes != nullptr;
     int head_end = 0;
 
@@ -321,7 +330,7 @@ attn_decode_q4_kernel(const DecodeQ4Params p)
         int min_lim = end;                               // every row sees the slots below it
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int r = r0 + 8 * nt + g;
+            const int r = r0 + row_of(8 * nt + g);
             uint32_t qv[NGK][8];
             uint32_t top = 0u;
 #pragma unroll
@@ -355,7 +364,7 @@ attn_decode_q4_kernel(const DecodeQ4Params p)
                 // scale * log2(e) * 2^(24 - e), kept finite and positive
                 ri.fac = fmaxf(fminf(p.scale_log2 * pow2i(24 - max(e, -100)) * pow2i(max(0, -100 - e)), 3e38f), 1.2e-38f);
                 __syncwarp();
-                if (t == 0) info[8 * nt + g] = ri;
+                if (t == 0) info[row_of(8 * nt + g)] = ri;
                 __syncwarp();
                 const float up = pow2i(e);
 #pragma unroll
@@ -387,14 +396,14 @@ attn_decode_q4_kernel(const DecodeQ4Params p)
                 }
             }
 #pragma unroll
-            for (int c = 0; c < 2; ++c) ef[nt][c] = biased ? 1.f : info[8 * nt + 2 * t + c].fac;
+            for (int c = 0; c < 2; ++c) ef[nt][c] = biased ? 1.f : info[row_of(8 * nt + 2 * t + c)].fac;
         }
         min_lim = __reduce_min_sync(0xffffffffu, min_lim);
 
-        float m_run[NT][2], l_run[NT][2], o[NT][NGV][4][4], zc[NT][4], rg[NGV];
+        float m_run[NT][2], l_run[NT][2], o[NT][NGV][4][4], zc[NT][4], rg[SETS];
         uint32_t thr = 0u;                               // the words whose s R stays below 2^15, per group
 #pragma unroll
-        for (int q = 0; q < NGV; ++q) rg[q] = 1.f;
+        for (int q = 0; q < SETS; ++q) rg[q] = 1.f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -474,7 +483,7 @@ attn_decode_q4_kernel(const DecodeQ4Params p)
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const RowInfo ri = info[8 * nt + 2 * t + c];
+                        const RowInfo ri = info[row_of(8 * nt + 2 * t + c)];
 #pragma unroll
                         for (int tile = 0; tile < 4; ++tile)
 #pragma unroll
@@ -489,7 +498,7 @@ attn_decode_q4_kernel(const DecodeQ4Params p)
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const int left = info[8 * nt + 2 * t + c].lim - key0 - pi;
+                        const int left = info[row_of(8 * nt + 2 * t + c)].lim - key0 - pi;
 #pragma unroll
                         for (int tile = 0; tile < 4; ++tile)
 #pragma unroll
@@ -591,21 +600,27 @@ attn_decode_q4_kernel(const DecodeQ4Params p)
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int c = 0; c < 2; ++c)
-                            if (poison >> (2 * nt + c) & 1u) zc[nt][2 * q + c] = __uint_as_float(0x7FC00000u);
+                            if ((poison >> (2 * nt + c) & 1u) && (!PACK || own_shift == 16 - 16 * q))
+                                zc[nt][PACK ? c : 2 * q + c] = __uint_as_float(0x7FC00000u);
                     if (big > ((thr >> (16 * q)) & 0xFFFFu)) {
                         const int ex = static_cast<int>(big >> 7) - 127;       // the largest s is in [2^ex, 2^(ex + 1))
                         const float r_new = pow2i(min(126, 12 - ex));
-                        const float f = r_new / rg[q];
-                        rg[q] = r_new;
                         thr = (thr & (q ? 0x0000FFFFu : 0xFFFF0000u)) | static_cast<uint32_t>((min(ex + 2 + 127, 254) << 7) | 0x7F) << (16 * q);
+                        if (!PACK || own_shift == 16 - 16 * q) {               // (PACK: not the other half of the columns)
+                            const float f = r_new / rg[PACK ? 0 : q];
+                            rg[PACK ? 0 : q] = r_new;
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            zc[nt][2 * q] *= f;
-                            zc[nt][2 * q + 1] *= f;
+                            for (int nt = 0; nt < NT; ++nt) {
+                                zc[nt][PACK ? 0 : 2 * q] *= f;
+                                zc[nt][PACK ? 1 : 2 * q + 1] *= f;
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
+                                for (int qq = 0; qq < NGV; ++qq)
 #pragma unroll
-                                for (int c = 0; c < 4; ++c) o[nt][q][j][c] *= f;
+                                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                                        for (int c = 0; c < 4; ++c)
+                                            if (PACK || qq == q) o[nt][qq][j][c] *= f;
+                            }
                         }
                     }
                 }
@@ -614,49 +629,53 @@ attn_decode_q4_kernel(const DecodeQ4Params p)
             // O^T += V^T (p s R)^T
 #pragma unroll
             for (int tile = 0; tile < 4; ++tile) {
-                uint32_t vc[4][NGV], vz[4];              // codes and words of slots t, t + 4, t + 8, t + 12 of the tile
+                uint32_t vc[4][NGV];                     // codes of slots t, t + 4, t + 8, t + 12 of the tile
                 const uint8_t* vb = sb + v_0 + tile * 16 * (DV / 2);
-                const uint8_t* zb = sb + vz_0 + tile * 16 * 2 * NGV;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     if (NGV == 2) {
                         const uint2 a = *reinterpret_cast<const uint2*>(vb + 4 * i * (DV / 2));
                         vc[i][0] = a.x;
                         vc[i][NGV - 1] = a.y;
-                        vz[i] = *reinterpret_cast<const uint32_t*>(zb + 4 * i * 2 * NGV);
                     } else {
                         vc[i][0] = *reinterpret_cast<const uint32_t*>(vb + 4 * i * (DV / 2));
-                        vz[i] = *reinterpret_cast<const uint16_t*>(zb + 4 * i * 2 * NGV);
                     }
                 }
+                uint32_t bp[SETS][NT][2];
 #pragma unroll
-                for (int q = 0; q < NGV; ++q) {
-                    const float s0 = word_step(vw[tile][0], q) * rg[q], s1 = word_step(vw[tile][1], q) * rg[q];
-                    uint32_t bp[NT][2];
+                for (int q = 0; q < SETS; ++q) {
+                    const int sh = q == 0 ? (PACK ? own_shift : 16) : 0;
+                    const float s0 = __uint_as_float((vw[tile][0] << sh) & 0xFFF00000u) * rg[q];
+                    const float s1 = __uint_as_float((vw[tile][1] << sh) & 0xFFF00000u) * rg[q];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        bp[nt][0] = transpose8(pack_f16x2(x[tile][nt][0] * s0, x[tile][nt][1] * s0));
-                        bp[nt][1] = transpose8(pack_f16x2(x[tile][nt][2] * s1, x[tile][nt][3] * s1));
+                        bp[q][nt][0] = transpose8(pack_f16x2(x[tile][nt][0] * s0, x[tile][nt][1] * s0));
+                        bp[q][nt][1] = transpose8(pack_f16x2(x[tile][nt][2] * s1, x[tile][nt][3] * s1));
                     }
-                    // the zeros: group 0's in the accumulator's rows 0-7, group 1's in 8-15
-                    const uint32_t z0 = __byte_perm(vz[0], vz[1], q ? 0x7632 : 0x5410) & LO;
-                    const uint32_t z1 = __byte_perm(vz[2], vz[3], q ? 0x7632 : 0x5410) & LO;
+                }
+                // the zeros: group 0's in the even rows, group 1's in the odd ones
+                const uint32_t z0 = transpose8(vw[tile][0] & LO), z1 = transpose8(vw[tile][1] & LO);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma_f16(zc[nt], q ? 0u : z0, q ? z0 : 0u, q ? 0u : z1, q ? z1 : 0u, bp[nt][0], bp[nt][1]);
+                for (int nt = 0; nt < NT; ++nt) {
+                    mma_f16(zc[nt], z0, 0u, z1, 0u, bp[0][nt][0], bp[0][nt][1]);
+                    if (SETS == 2) mma_f16(zc[nt], 0u, z0, 0u, z1, bp[SETS - 1][nt][0], bp[SETS - 1][nt][1]);
+                }
+#pragma unroll
+                for (int q = 0; q < NGV; ++q)
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf) {     // codes 4 hf .. 4 hf + 3 of both slots of a pair
                         const uint32_t a = __byte_perm(vc[0][q], vc[1][q], hf ? 0x7632 : 0x5410);
                         const uint32_t c = __byte_perm(vc[2][q], vc[3][q], hf ? 0x7632 : 0x5410);
 #pragma unroll
-                        for (int jj = 0; jj < 2; ++jj) {
-                            const uint32_t as = a >> (8 * jj), cs = c >> (8 * jj);
+                        for (int jj = 0; jj < 2; ++jj) { // even channel: the nibble; odd channel: the byte
+                            const uint32_t ab = jj ? __byte_perm(a, 0u, 0x4341) : a & 0x00FF00FFu;
+                            const uint32_t cb = jj ? __byte_perm(c, 0u, 0x4341) : c & 0x00FF00FFu;
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
-                                mma_f16(o[nt][q][2 * hf + jj], as & LO, as & HI, cs & LO, cs & HI, bp[nt][0], bp[nt][1]);
+                                mma_f16(o[nt][q][2 * hf + jj], ab & LO, ab, cb & LO, cb, bp[PACK ? 0 : q][nt][0],
+                                        bp[PACK ? 0 : q][nt][1]);
                         }
                     }
-                }
             }
             ++landed;
             __syncwarp();                                // every lane is done with the stage
@@ -672,24 +691,31 @@ attn_decode_q4_kernel(const DecodeQ4Params p)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const int row = 8 * nt + 2 * t + c;
+                const int row = row_of(8 * nt + 2 * t + c);
                 float l = l_run[nt][c];
 #pragma unroll
                 for (int sh = 4; sh < 32; sh <<= 1) l += __shfl_xor_sync(0xffffffffu, l, sh);
+                // the zeros' sums of a group lie in the lanes with g even (0) or odd (1)
+                float z[NGV];
+#pragma unroll
+                for (int q = 0; q < NGV; ++q) z[q] = __shfl_sync(0xffffffffu, zc[nt][PACK ? c : 2 * q + c], (lane & ~4) | 4 * q);
                 if (row >= rows) continue;
                 const float m_use = m_run[nt][c] == -INFINITY ? 0.f : m_run[nt][c];
                 const int64_t orow = pair_bh * p.R + r0 + row;
                 // (a NaN sum is not 0: it reaches the output)
                 const float inv_l = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
 #pragma unroll
-                for (int q = 0; q < NGV; ++q) {
-                    const float f = inv_l / rg[q];
+                for (int k = 0; k < SETS; ++k) {
+                    const int q = PACK ? t >> 1 : k;     // (PACK: the group of these columns)
+                    const float f = inv_l / rg[k];
+                    const float zq = PACK && q == 1 ? z[NGV - 1] : z[k];
                     float v[8];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        // (u0 2^-24 as the even channels' u)
-                        v[2 * j] = (o[nt][q][j][c] - zc[nt][2 * q + c]) * TWO24 * f;
-                        v[2 * j + 1] = fmaf(o[nt][q][j][c + 2], TWO20, -zc[nt][2 * q + c] * TWO24) * f;
+                        const float ev = PACK && q == 1 ? o[nt][NGV - 1][j][c] : o[nt][k][j][c];
+                        const float both = PACK && q == 1 ? o[nt][NGV - 1][j][c + 2] : o[nt][k][j][c + 2];
+                        v[2 * j] = (ev - zq) * TWO24 * f;
+                        v[2 * j + 1] = fmaf(both - ev, TWO20, -zq * TWO24) * f;
                     }
                     if (whole) {
                         uint4 w;
@@ -704,7 +730,7 @@ attn_decode_q4_kernel(const DecodeQ4Params p)
                         dst[1] = make_float4(v[4], v[5], v[6], v[7]);
                     }
                 }
-                if (g == 0) {
+                if (g == 0 && (!PACK || t < 2)) {
                     if (!whole) {
                         *reinterpret_cast<float2*>(p.part_ml + 2 * (part0 + row)) = make_float2(m_run[nt][c], l);
                     } else if (p.LSE != nullptr) {
@@ -814,11 +840,11 @@ attn_decode_q4_merge_kernel(const DecodeQ4Params p, int tile_rows)
     if (threadIdx.x == 0 && p.LSE != nullptr) p.LSE[orow] = Lsum == 0.f ? -INFINITY : (M_use + __log2f(Lsum)) * LN2;
 }
 
-template <int DK, int DV, int NT>
+template <int DK, int DV, int NT, bool PACK>
 cudaError_t launch(const DecodeQ4Params& p, cudaStream_t stream)
 {
-    using L = Layout<DK, DV, NT>;
-    auto kern = attn_decode_q4_kernel<DK, DV, NT>;
+    using L = Layout<DK, DV, NT, PACK>;
+    auto kern = attn_decode_q4_kernel<DK, DV, NT, PACK>;
     static bool configured[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
