@@ -1135,7 +1135,7 @@ extern "C" int attn_decode_q4(const void* Q, const void* cache, int B, int H, in
     const Q4Plan w = q4_plan(B, H, H_kv, n, m, d_k, d_v);
     if (w.total > 0 && (workspace == nullptr || workspace_bytes < w.total)) return ATTN_ERR_INVALID_ARG;
     if (w.total > 0 && !aligned(workspace, kWsAlign)) return ATTN_ERR_MISALIGNED;
-    if (w.few && w.pairs * q4_blocks(m) > INT32_MAX) return ATTN_ERR_UNSUPPORTED;
+    if (w.few && (w.pairs * q4_blocks(m) > INT32_MAX || w.pairs * w.part_rows > INT32_MAX)) return ATTN_ERR_UNSUPPORTED;
     uint32_t* status = nullptr;
     if ((rc = status_word(&status)) != ATTN_OK) return rc;
     uint8_t* wsb = static_cast<uint8_t*>(workspace);
@@ -1178,6 +1178,9 @@ extern "C" int attn_decode_q4(const void* Q, const void* cache, int B, int H, in
     p.pair_first = reinterpret_cast<int*>(wsb + w.first_off);
     p.part_ends = reinterpret_cast<int*>(wsb + w.ends_off);
     p.part_rows = w.part_rows;
+    // about four parts to a warp of the merge
+    const int64_t parts = (p.warps + w.pairs - 1) / w.pairs + 1;
+    p.merge_warps = parts <= 4 ? 1 : parts <= 8 ? 2 : parts <= 16 ? 4 : 8;
     p.status = status;
     p.watchdog_ns = g_watchdog_ns;
     p.debug_flags = g_debug_flags;

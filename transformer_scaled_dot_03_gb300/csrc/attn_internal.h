@@ -187,6 +187,7 @@ struct DecodeQ4Params {
     int* pair_first;              // [pairs]: the worker whose slot 1 holds a cut pair's first part, -1 for a whole pair
     int* part_ends;               // [warps]: whether the worker's slot 0 is the last part of its pair
     int part_rows;
+    int merge_warps;              // warps of the merge kernel per (pair, row): 1, 2, 4 or 8
     uint32_t* status;
     uint64_t watchdog_ns;
     uint32_t debug_flags;

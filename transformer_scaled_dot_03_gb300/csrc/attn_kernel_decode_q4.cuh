@@ -430,7 +430,7 @@ attn_decode_q4_kernel(const DecodeQ4Params p)
             if (!ok) break;
             const uint8_t* sb = smem + (warp * L::STAGES + stage) * L::BYTES_BLOCK;
             const int key0 = blk * q4::BLOCK;
-            const bool masked = key0 + q4::BLOCK > min_lim;
+            const bool masked = __any_sync(0xffffffffu, key0 + q4::BLOCK > min_lim);   // (a vote, so a branch)
 
             // raw scores
             float x[4][NT][4];
@@ -758,10 +758,10 @@ attn_decode_q4_kernel(const DecodeQ4Params p)
     if (p.split && lane == 0) p.part_ends[worker] = head_end;
 }
 
-// Merge of the parts of the cut pairs: CTA (pair, row), the parts dealt out to its
-// warps. The first part is slot 1 of worker pair_first[pair]; the parts after it are the
-// slots 0 of the workers that follow, up to the one that ends the pair.
-constexpr int MERGE_WARPS = 8;
+// Merge of the parts of the cut pairs, p.merge_warps warps to each (pair, row). The
+// first part is slot 1 of worker pair_first[pair]; the parts after it are the slots 0 of
+// the workers that follow, up to the one that ends the pair.
+constexpr int MERGE_WARPS = 8;                           // per CTA
 
 template <int DV>
 __global__ void __launch_bounds__(32 * MERGE_WARPS)
@@ -770,74 +770,80 @@ attn_decode_q4_merge_kernel(const DecodeQ4Params p, int tile_rows)
     constexpr int CPL = DV / 32;
     __shared__ float red[MERGE_WARPS][DV];
     griddep_wait();   // the parts are visible
-    const int64_t pair = blockIdx.x;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int first = p.pair_first[pair];
-    if (first < 0 || first >= p.warps) return;           // whole
-    const int row = static_cast<int>(blockIdx.y);
-    const int64_t pair_bh = pair / p.row_tiles;
+    const int wpr = p.merge_warps, sub = warp & (wpr - 1);
+    const uint32_t item = blockIdx.x * static_cast<uint32_t>(MERGE_WARPS / wpr) + warp / wpr;
+    const uint32_t pair = item / static_cast<uint32_t>(p.part_rows);
+    const int row = static_cast<int>(item - pair * p.part_rows);
+    const uint32_t pair_bh = pair / static_cast<uint32_t>(p.row_tiles);
     const int r = static_cast<int>(pair - pair_bh * p.row_tiles) * tile_rows + row;
-    if (r >= p.R) return;
-    // worker first + s has part s; lane l looks at parts l, l + 32, ... until one ends the pair
-    auto part_row = [&](int s) -> int64_t {
-        return static_cast<int64_t>(s == 0 ? 2 * first + 1 : 2 * (first + s)) * p.part_rows + row;
-    };
-    int parts = 0;
-    float M = -INFINITY, Lsum = 0.f;
-    for (int base = 0;; base += 32) {
-        const int s = base + lane;
-        const bool there = first + s < p.warps;
-        const float2 ml = there ? *reinterpret_cast<const float2*>(p.part_ml + 2 * part_row(s)) : make_float2(-INFINITY, 0.f);
-        const uint32_t ends = __ballot_sync(0xffffffffu, !there || (s > 0 && p.part_ends[first + s] != 0));
-        const int n = ends != 0u ? __ffs(ends) : 32;     // parts of these 32
-        float m = lane < n ? ml.x : -INFINITY, l = lane < n ? ml.y : 0.f;
-        const float mine = m;
-#pragma unroll
-        for (int sh = 16; sh > 0; sh >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, sh));
-        const float m_new = fmaxf(M, m), m_use = m_new == -INFINITY ? 0.f : m_new;
-        l = lane < n ? l * ex2_approx(mine - m_use) : 0.f;
-#pragma unroll
-        for (int sh = 16; sh > 0; sh >>= 1) l += __shfl_xor_sync(0xffffffffu, l, sh);
-        Lsum = fmaf(Lsum, ex2_approx(M - m_use), l);
-        M = m_new;
-        parts += n;
-        if (ends != 0u) break;
-    }
-    parts = min(parts, p.warps - first);
-    const float M_use = M == -INFINITY ? 0.f : M;
-    float acc[CPL];
+    const bool there = pair_bh < static_cast<uint32_t>(p.B) * p.H_kv && r < p.R;
+    const int first = there ? p.pair_first[pair] : -1;
+    const bool live = first >= 0 && first < p.warps;     // else whole (or past the last pair)
+    float M_use = 0.f, Lsum = 0.f, acc[CPL];
 #pragma unroll
     for (int c = 0; c < CPL; ++c) acc[c] = 0.f;
+    if (live) {
+        // worker first + s has part s; lane l looks at parts l, l + 32, ... until one ends the pair
+        auto part_row = [&](int s) -> int64_t {
+            return static_cast<int64_t>(s == 0 ? 2 * first + 1 : 2 * (first + s)) * p.part_rows + row;
+        };
+        int parts = 0;
+        float M = -INFINITY;
+        for (int base = 0;; base += 32) {
+            const int s = base + lane;
+            const bool some = first + s < p.warps;
+            const float2 ml = some ? *reinterpret_cast<const float2*>(p.part_ml + 2 * part_row(s)) : make_float2(-INFINITY, 0.f);
+            const uint32_t ends = __ballot_sync(0xffffffffu, !some || (s > 0 && p.part_ends[first + s] != 0));
+            const int n = ends != 0u ? __ffs(ends) : 32; // parts of these 32
+            const float mine = lane < n ? ml.x : -INFINITY;
+            float m = mine;
+#pragma unroll
+            for (int sh = 16; sh > 0; sh >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, sh));
+            const float m_new = fmaxf(M, m), m_ref = m_new == -INFINITY ? 0.f : m_new;
+            float l = lane < n ? ml.y * ex2_approx(mine - m_ref) : 0.f;
+#pragma unroll
+            for (int sh = 16; sh > 0; sh >>= 1) l += __shfl_xor_sync(0xffffffffu, l, sh);
+            Lsum = fmaf(Lsum, ex2_approx(M - m_ref), l);
+            M = m_new;
+            parts += n;
+            if (ends != 0u) break;
+        }
+        parts = min(parts, p.warps - first);
+        M_use = M == -INFINITY ? 0.f : M;
 #pragma unroll 8
-    for (int s = warp; s < parts; s += MERGE_WARPS) {
-        const int64_t pr = part_row(s);
-        const float f = ex2_approx(p.part_ml[2 * pr] - M_use);
-        if (CPL == 4) {
-            const float4 v = *reinterpret_cast<const float4*>(p.part_o + pr * DV + 4 * lane);
-            acc[0] = fmaf(v.x, f, acc[0]);
-            acc[1] = fmaf(v.y, f, acc[1]);
-            acc[CPL - 2] = fmaf(v.z, f, acc[CPL - 2]);
-            acc[CPL - 1] = fmaf(v.w, f, acc[CPL - 1]);
-        } else {
-            const float2 v = *reinterpret_cast<const float2*>(p.part_o + pr * DV + 2 * lane);
-            acc[0] = fmaf(v.x, f, acc[0]);
-            acc[1] = fmaf(v.y, f, acc[1]);
+        for (int s = sub; s < parts; s += wpr) {
+            const int64_t pr = part_row(s);
+            const float f = ex2_approx(p.part_ml[2 * pr] - M_use);
+            if (CPL == 4) {
+                const float4 v = *reinterpret_cast<const float4*>(p.part_o + pr * DV + 4 * lane);
+                acc[0] = fmaf(v.x, f, acc[0]);
+                acc[1] = fmaf(v.y, f, acc[1]);
+                acc[CPL - 2] = fmaf(v.z, f, acc[CPL - 2]);
+                acc[CPL - 1] = fmaf(v.w, f, acc[CPL - 1]);
+            } else {
+                const float2 v = *reinterpret_cast<const float2*>(p.part_o + pr * DV + 2 * lane);
+                acc[0] = fmaf(v.x, f, acc[0]);
+                acc[1] = fmaf(v.y, f, acc[1]);
+            }
         }
     }
+    if (wpr > 1) {
 #pragma unroll
-    for (int c = 0; c < CPL; ++c) red[warp][CPL * lane + c] = acc[c];
-    __syncthreads();
-    const int64_t orow = pair_bh * p.R + r;
-    const float inv = Lsum == 0.f ? 0.f : 1.f / Lsum;
-    if (threadIdx.x < DV / 2) {
-        float v[2] = {0.f, 0.f};
+        for (int c = 0; c < CPL; ++c) red[warp][CPL * lane + c] = acc[c];
+        __syncthreads();
+        if (sub == 0)
+            for (int w = 1; w < wpr; ++w)
 #pragma unroll
-        for (int w = 0; w < MERGE_WARPS; ++w)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) v[h] += red[w][2 * threadIdx.x + h];
-        *reinterpret_cast<uint32_t*>(p.O + orow * DV + 2 * threadIdx.x) = pack_bf16x2(v[0] * inv, v[1] * inv);
+                for (int c = 0; c < CPL; ++c) acc[c] += red[warp + w][CPL * lane + c];
     }
-    if (threadIdx.x == 0 && p.LSE != nullptr) p.LSE[orow] = Lsum == 0.f ? -INFINITY : (M_use + __log2f(Lsum)) * LN2;
+    if (!live || sub != 0) return;
+    const int64_t orow = static_cast<int64_t>(pair_bh) * p.R + r;
+    const float inv = Lsum == 0.f ? 0.f : 1.f / Lsum;
+#pragma unroll
+    for (int c = 0; c < CPL; c += 2)
+        *reinterpret_cast<uint32_t*>(p.O + orow * DV + CPL * lane + c) = pack_bf16x2(acc[c] * inv, acc[c + 1] * inv);
+    if (lane == 0 && p.LSE != nullptr) p.LSE[orow] = Lsum == 0.f ? -INFINITY : (M_use + __log2f(Lsum)) * LN2;
 }
 
 template <int DK, int DV, int NT, bool PACK>
@@ -858,8 +864,9 @@ cudaError_t launch(const DecodeQ4Params& p, cudaStream_t stream)
     const unsigned ctas = static_cast<unsigned>((p.warps + WARPS - 1) / WARPS);
     e = launch_pdl(kern, dim3(ctas), dim3(THREADS), L::BYTES, stream, p);
     if (e != cudaSuccess || !p.split) return e;
-    const unsigned pairs = static_cast<unsigned>(static_cast<int64_t>(p.B) * p.H_kv * p.row_tiles);
-    return launch_pdl(attn_decode_q4_merge_kernel<DV>, dim3(pairs, static_cast<unsigned>(p.part_rows)),
+    const int64_t items = static_cast<int64_t>(p.B) * p.H_kv * p.row_tiles * p.part_rows;
+    const int per = MERGE_WARPS / p.merge_warps;
+    return launch_pdl(attn_decode_q4_merge_kernel<DV>, dim3(static_cast<unsigned>((items + per - 1) / per)),
                       dim3(32 * MERGE_WARPS), 0, stream, p, L::ROWS);
 }
 
