@@ -993,7 +993,7 @@ struct Q4Plan {
     int rows, row_tiles;              // rows per cache head, tiles of them
     int64_t pairs, warps;             // (b, cache head, row tile) triples; most workers
     int part_rows;
-    size_t ml_off, first_off, ends_off;   // split
+    size_t ml_off, pairs_off;         // split
     size_t v_off;                     // many rows
     size_t total;
 };
@@ -1019,9 +1019,8 @@ Q4Plan q4_plan(int64_t B, int64_t H, int64_t H_kv, int64_t n, int m, int d_k, in
     w.part_rows = std::min(w.rows, tile);
     const size_t parts = static_cast<size_t>(2 * w.warps) * w.part_rows;
     w.ml_off = round_up(parts * d_v * 4, kWsAlign);
-    w.first_off = w.ml_off + round_up(parts * 2 * 4, kWsAlign);
-    w.ends_off = w.first_off + round_up(static_cast<size_t>(w.pairs) * 4, kWsAlign);
-    w.total = w.ends_off + round_up(static_cast<size_t>(w.warps) * 4, kWsAlign);
+    w.pairs_off = w.ml_off + round_up(parts * 2 * 4, kWsAlign);
+    w.total = w.pairs_off + round_up(static_cast<size_t>(w.pairs) * 8, kWsAlign);
     return w;
 }
 
@@ -1135,7 +1134,7 @@ extern "C" int attn_decode_q4(const void* Q, const void* cache, int B, int H, in
     const Q4Plan w = q4_plan(B, H, H_kv, n, m, d_k, d_v);
     if (w.total > 0 && (workspace == nullptr || workspace_bytes < w.total)) return ATTN_ERR_INVALID_ARG;
     if (w.total > 0 && !aligned(workspace, kWsAlign)) return ATTN_ERR_MISALIGNED;
-    if (w.few && (w.pairs * q4_blocks(m) > INT32_MAX || w.pairs * w.part_rows > INT32_MAX)) return ATTN_ERR_UNSUPPORTED;
+    if (w.few && (w.pairs * (q4_blocks(m) + 1) > INT32_MAX || w.pairs * w.part_rows > INT32_MAX)) return ATTN_ERR_UNSUPPORTED;
     uint32_t* status = nullptr;
     if ((rc = status_word(&status)) != ATTN_OK) return rc;
     uint8_t* wsb = static_cast<uint8_t*>(workspace);
@@ -1175,8 +1174,7 @@ extern "C" int attn_decode_q4(const void* Q, const void* cache, int B, int H, in
     p.LSE = LSE;
     p.part_o = reinterpret_cast<float*>(wsb);
     p.part_ml = reinterpret_cast<float*>(wsb + w.ml_off);
-    p.pair_first = reinterpret_cast<int*>(wsb + w.first_off);
-    p.part_ends = reinterpret_cast<int*>(wsb + w.ends_off);
+    p.pair_parts = reinterpret_cast<int2*>(wsb + w.pairs_off);
     p.part_rows = w.part_rows;
     // about four parts to a warp of the merge
     const int64_t parts = (p.warps + w.pairs - 1) / w.pairs + 1;

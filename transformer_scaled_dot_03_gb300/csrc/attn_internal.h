@@ -184,8 +184,7 @@ struct DecodeQ4Params {
     float* LSE;                   // fp32 [B,H,n] or null
     float* part_o;                // fp32 [2 warps][part_rows][d_v] (split)
     float* part_ml;               // fp32 [2 warps][part_rows][2]: max (log2 domain), sum
-    int* pair_first;              // [pairs]: the worker whose slot 1 holds a cut pair's first part, -1 for a whole pair
-    int* part_ends;               // [warps]: whether the worker's slot 0 is the last part of its pair
+    int2* pair_parts;             // [pairs]: first and last worker of a cut pair, (-1, 0) for a whole one
     int part_rows;
     int merge_warps;              // warps of the merge kernel per (pair, row): 1, 2, 4 or 8
     uint32_t* status;

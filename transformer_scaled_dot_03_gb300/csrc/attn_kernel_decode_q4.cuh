@@ -37,15 +37,18 @@
 // in registers). Row r of a 16-slot tile is slot 4 (r % 2) + (r % 8) / 2 + 8 (r / 8), so that
 // a thread's four V slots are t, t + 4, t + 8, t + 12 and a warp reads 16 contiguous rows.
 //
-// Every warp is a worker of its own: the blocks of all (entry, cache head, row tile)
-// pairs, as the entries' lengths have them on the device, form one sequence, and of T
-// blocks warp w of W takes [T w / W, T (w + 1) / W), streaming them through its own ring
-// (lane 0 issues a bulk copy per block as soon as the warp has consumed a stage, across
-// the pairs' ends) with an online softmax of its own. A pair that lies in one warp's
-// range is written there; of one that is cut, each warp writes its part (max, sum,
-// unnormalised O) to its slot 0 (the pair began in an earlier warp) or slot 1, and a
-// second kernel merges the parts in order. (A CTA per pair, its warps merging in
-// shared memory, spent 6 us per pair on latencies that nothing covered.)
+// Every warp is a worker of its own. The blocks of all (entry, cache head, row tile)
+// pairs, as the entries' lengths have them on the device, form one sequence, each
+// pair preceded by one more unit for what its start costs a warp (2.9 us: query rows,
+// fresh state, output; a block takes 2.2). Of T units warp w of W takes
+// [T w / W, T (w + 1) / W), streaming its blocks through its own ring (lane 0 issues a
+// bulk copy per block as soon as the warp has consumed a stage, across the pairs' ends)
+// with an online softmax of its own. A pair that lies in one warp's range is written there;
+// of one that is cut, each warp writes its part (max, sum, unnormalised O) to its slot 0
+// (the pair began in an earlier warp) or slot 1, and a second kernel merges the parts in
+// order. (A CTA per pair, its warps merging in shared memory, spent 6 us per pair on
+// latencies that nothing covered; chunks that an SM's warps take in turn cost more in
+// pair starts than the better balance gives.)
 #pragma once
 
 #include <cstdint>
@@ -158,32 +161,48 @@ __device__ __forceinline__ int pair_blocks(const DecodeQ4Params& p, int b)
     return max(1, (visible_end(p, b, &kv) + q4::BLOCK - 1) / q4::BLOCK);
 }
 
-// A place in the sequence of blocks: block blk of nb of pair pr of entry b, and the
-// units left to take (blocks, or whole pairs without `split`).
+// A place in the sequence: block blk of nb of pair pr of entry b, whose pairs begin at
+// unit `before`; units left to take (with `split` blocks and pair starts, else pairs).
 struct Cursor {
     int b, pr, blk, nb, todo;
+    uint32_t before;
 
-    __device__ __forceinline__ void next(const DecodeQ4Params& p, int pairs_b)
+    // Past `blocks` blocks of the pair.
+    __device__ __forceinline__ void next(const DecodeQ4Params& p, int pairs_b, int blocks)
     {
-        if (p.split) --todo;
-        if (++blk < nb) return;
-        if (!p.split) --todo;
+        if (p.split) todo -= blocks;
+        blk += blocks;
+        if (blk < nb) return;
+        --todo;                                          // the next pair's start, or the pair itself
         blk = 0;
         if (++pr == pairs_b) {
             pr = 0;
+            before += static_cast<uint32_t>(p.split ? nb + 1 : 1) * pairs_b;
             ++b;
             if (todo > 0) nb = pair_blocks(p, b);
         }
     }
 };
 
+// Worker w's units are [each w + min(w, more), ...), each of them or one more.
+struct Shares {
+    uint32_t each, more;
+
+    __device__ __forceinline__ uint32_t worker_of(uint32_t u) const
+    {
+        const uint32_t wide = more * (each + 1u);
+        return u < wide ? u / (each + 1u) : more + (u - wide) / max(each, 1u);
+    }
+};
+
 // Worker w's share of the sequence (idle workers, where there are fewer units than
 // workers, come last).
-__device__ __forceinline__ Cursor first_block(const DecodeQ4Params& p, int w, int lane, int pairs_b)
+__device__ __forceinline__ Cursor first_block(const DecodeQ4Params& p, int w, int lane, int pairs_b, Shares* shares)
 {
     Cursor c;
     c.b = c.pr = c.blk = 0;
     c.nb = 1;
+    c.before = 0;
     constexpr int HELD = 4;                              // entries per lane that are looked at once
     int nb[HELD];
     const bool ragged = p.split && mask_has_lengths(p.mask);
@@ -193,34 +212,34 @@ __device__ __forceinline__ Cursor first_block(const DecodeQ4Params& p, int w, in
 #pragma unroll
         for (int k = 0; k < HELD; ++k) {
             const int i = 32 * k + lane;
-            nb[k] = i < p.B ? pair_blocks(p, i) * pairs_b : 0;
+            nb[k] = i < p.B ? (pair_blocks(p, i) + 1) * pairs_b : 0;
             sum += nb[k];
         }
-        for (int i = 32 * HELD + lane; i < p.B; i += 32) sum += pair_blocks(p, i) * pairs_b;
+        for (int i = 32 * HELD + lane; i < p.B; i += 32) sum += (pair_blocks(p, i) + 1) * pairs_b;
         total = __reduce_add_sync(0xffffffffu, sum);
     } else {
-        total = static_cast<uint32_t>(p.B) * pairs_b * (p.split ? pair_blocks(p, 0) : 1);
+        total = static_cast<uint32_t>(p.B) * pairs_b * (p.split ? pair_blocks(p, 0) + 1 : 1);
     }
-    const uint32_t each = total / p.warps, more = total - each * p.warps;
-    uint32_t u0 = each * w + min(static_cast<uint32_t>(w), more);
-    c.todo = static_cast<int>(each + (static_cast<uint32_t>(w) < more ? 1u : 0u));
+    shares->each = total / p.warps;
+    shares->more = total - shares->each * p.warps;
+    uint32_t u0 = shares->each * w + min(static_cast<uint32_t>(w), shares->more);
+    c.todo = static_cast<int>(shares->each + (static_cast<uint32_t>(w) < shares->more ? 1u : 0u));
     if (c.todo == 0) return c;
     if (!p.split) {
         c.b = static_cast<int>(u0 / pairs_b);
-        c.pr = static_cast<int>(u0 - static_cast<uint32_t>(c.b) * pairs_b);
+        c.before = static_cast<uint32_t>(c.b) * pairs_b;
+        c.pr = static_cast<int>(u0 - c.before);
         c.nb = pair_blocks(p, c.b);
         return c;
     }
     if (ragged) {
-        int units = 0;
-        uint32_t before = 0;                             // units of the entries before the 32 looked at
         for (int base = 0;; base += 32) {
-            units = 0;
+            int units = 0;
             if (base < 32 * HELD) {
 #pragma unroll
                 for (int k = 0; k < HELD; ++k) units = base == 32 * k ? nb[k] : units;
             } else if (base + lane < p.B) {
-                units = pair_blocks(p, base + lane) * pairs_b;
+                units = (pair_blocks(p, base + lane) + 1) * pairs_b;
             }
             uint32_t incl = units;
 #pragma unroll
@@ -228,24 +247,30 @@ __device__ __forceinline__ Cursor first_block(const DecodeQ4Params& p, int w, in
                 const uint32_t v = __shfl_up_sync(0xffffffffu, incl, off);
                 if (lane >= off) incl += v;
             }
-            const uint32_t past = __ballot_sync(0xffffffffu, before + incl > u0);
+            const uint32_t past = __ballot_sync(0xffffffffu, c.before + incl > u0);
             if (past != 0u) {
                 const int l = __ffs(past) - 1;
                 c.b = base + l;
-                u0 -= before + __shfl_sync(0xffffffffu, incl - units, l);
-                c.nb = __shfl_sync(0xffffffffu, units, l) / pairs_b;
+                c.before += __shfl_sync(0xffffffffu, incl - units, l);
+                c.nb = __shfl_sync(0xffffffffu, units, l) / pairs_b - 1;
                 break;
             }
-            before += __shfl_sync(0xffffffffu, incl, 31);
+            c.before += __shfl_sync(0xffffffffu, incl, 31);
+            if (base + 32 >= p.B) break;                 // (never: u0 is below the total)
         }
     } else {
         c.nb = pair_blocks(p, 0);
-        const uint32_t per = static_cast<uint32_t>(pairs_b) * c.nb;
+        const uint32_t per = static_cast<uint32_t>(pairs_b) * (c.nb + 1);
         c.b = static_cast<int>(u0 / per);
-        u0 -= per * c.b;
+        c.before = per * c.b;
     }
-    c.pr = static_cast<int>(u0) / c.nb;
-    c.blk = static_cast<int>(u0) - c.pr * c.nb;
+    u0 -= c.before;
+    c.pr = static_cast<int>(u0) / (c.nb + 1);
+    c.blk = static_cast<int>(u0) - c.pr * (c.nb + 1) - 1;
+    if (c.blk < 0) {                                     // the share begins with the pair's start
+        c.blk = 0;
+        --c.todo;
+    }
     return c;
 }
 
@@ -279,7 +304,8 @@ attn_decode_q4_kernel(const DecodeQ4Params p)
     const int worker = warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
     if (worker >= p.warps) return;
     const int pairs_b = p.H_kv * p.row_tiles;            // pairs per entry
-    Cursor at = first_block(p, worker, lane, pairs_b);
+    Shares shares;
+    Cursor at = first_block(p, worker, lane, pairs_b, &shares);
     Cursor ahead = at;                                   // the next block to copy
     uint32_t landed = 0, issued = 0;                     // blocks consumed, copies issued
     auto issue = [&]() {
@@ -290,15 +316,16 @@ attn_decode_q4_kernel(const DecodeQ4Params p)
             bulk_load(ring + s * L::BYTES_BLOCK, p.cache + block * L::BYTES_BLOCK, L::BYTES_BLOCK, bar0 + 8u * s);
         }
         ++issued;
-        ahead.next(p, pairs_b);
+        ahead.next(p, pairs_b, 1);
     };
     bool ok = true;
     if (p.debug_flags & DEBUG_FORCE_TIMEOUT) {
         ok = mbar_wait(bar_never, 0, abort_word, p.status, STATUS_FORCED, 20000000ull);
         ok = __all_sync(0xffffffffu, ok);
     }
-    if (ok)
-        while (issued < L::STAGES && ahead.todo > 0) issue();
+    // one block now, the others of the ring behind the first query rows: so every warp's
+    // first block comes early
+    if (ok && ahead.todo > 0) issue();
 
     const int pi = 4 * (g & 1) + (g >> 1);               // slot of tile row g inside a 16-slot tile
     // byte offsets of this thread's codes and words inside a block
@@ -308,7 +335,6 @@ attn_decode_q4_kernel(const DecodeQ4Params p)
     auto row_of = [](int column) { return PACK ? column & 3 : column; };
     const int own_shift = PACK && t >= 2 ? 0 : 16;       // brings the step of set 0 in a word to the upper half
     const bool biased = p.slopes != nullptr;
-    int head_end = 0;
 
     while (ok && at.todo > 0) {
         // -------------------------------------------- a pair (or this warp's part of one)
@@ -399,6 +425,7 @@ attn_decode_q4_kernel(const DecodeQ4Params p)
             for (int c = 0; c < 2; ++c) ef[nt][c] = biased ? 1.f : info[row_of(8 * nt + 2 * t + c)].fac;
         }
         min_lim = __reduce_min_sync(0xffffffffu, min_lim);
+        while (landed == 0 && issued < L::STAGES && ahead.todo > 0) issue();
 
         float m_run[NT][2], l_run[NT][2], o[NT][NGV][4][4], zc[NT][4], rg[SETS];
         uint32_t thr = 0u;                               // the words whose s R stays below 2^15, per group
@@ -738,15 +765,12 @@ attn_decode_q4_kernel(const DecodeQ4Params p)
                     }
                 }
             }
-        if (p.split && lane == 0 && !mid_pair) p.pair_first[pair] = whole ? -1 : worker;
-        if (mid_pair && ends) head_end = 1;
-        at.todo -= p.split ? last - at.blk : 1;
-        at.blk = 0;
-        if (++at.pr == pairs_b) {
-            at.pr = 0;
-            ++at.b;
-            if (at.todo > 0) at.nb = pair_blocks(p, at.b);
+        if (p.split && lane == 0 && !mid_pair) {
+            // (the pair's last block is unit nb of it)
+            const uint32_t u = at.before + static_cast<uint32_t>(at.pr) * (nb + 1) + nb;
+            p.pair_parts[pair] = whole ? make_int2(-1, 0) : make_int2(worker, static_cast<int>(shares.worker_of(u)));
         }
+        at.next(p, pairs_b, last - at.blk);
     }
     if (!ok) {
         // land what is still in flight before the CTA's shared memory is given up
@@ -755,12 +779,10 @@ attn_decode_q4_kernel(const DecodeQ4Params p)
             while (!mbar_test(bar0 + 8u * (i % L::STAGES), (i / L::STAGES) & 1u) && globaltimer_ns() - t0 < 100000000ull) {
             }
     }
-    if (p.split && lane == 0) p.part_ends[worker] = head_end;
 }
 
-// Merge of the parts of the cut pairs, p.merge_warps warps to each (pair, row). The
-// first part is slot 1 of worker pair_first[pair]; the parts after it are the slots 0 of
-// the workers that follow, up to the one that ends the pair.
+// Merge of the parts of the cut pairs, p.merge_warps warps to each (pair, row): slot 1 of
+// worker pair_parts[pair].x, then the slots 0 of the workers after it up to pair_parts[pair].y.
 constexpr int MERGE_WARPS = 8;                           // per CTA
 
 template <int DV>
@@ -778,66 +800,70 @@ attn_decode_q4_merge_kernel(const DecodeQ4Params p, int tile_rows)
     const uint32_t pair_bh = pair / static_cast<uint32_t>(p.row_tiles);
     const int r = static_cast<int>(pair - pair_bh * p.row_tiles) * tile_rows + row;
     const bool there = pair_bh < static_cast<uint32_t>(p.B) * p.H_kv && r < p.R;
-    const int first = there ? p.pair_first[pair] : -1;
-    const bool live = first >= 0 && first < p.warps;     // else whole (or past the last pair)
-    float M_use = 0.f, Lsum = 0.f, acc[CPL];
+    const int2 span = there ? p.pair_parts[pair] : make_int2(-1, 0);
+    const bool live = span.x >= 0 && span.y > span.x && span.y < p.warps;      // else whole (or past the last pair)
+    float M = -INFINITY, Lsum = 0.f, acc[CPL];
 #pragma unroll
     for (int c = 0; c < CPL; ++c) acc[c] = 0.f;
     if (live) {
-        // worker first + s has part s; lane l looks at parts l, l + 32, ... until one ends the pair
+        const int n = span.y - span.x + 1;
         auto part_row = [&](int s) -> int64_t {
-            return static_cast<int64_t>(s == 0 ? 2 * first + 1 : 2 * (first + s)) * p.part_rows + row;
+            return static_cast<int64_t>(s == 0 ? 2 * span.x + 1 : 2 * (span.x + s)) * p.part_rows + row;
         };
-        int parts = 0;
-        float M = -INFINITY;
-        for (int base = 0;; base += 32) {
-            const int s = base + lane;
-            const bool some = first + s < p.warps;
-            const float2 ml = some ? *reinterpret_cast<const float2*>(p.part_ml + 2 * part_row(s)) : make_float2(-INFINITY, 0.f);
-            const uint32_t ends = __ballot_sync(0xffffffffu, !some || (s > 0 && p.part_ends[first + s] != 0));
-            const int n = ends != 0u ? __ffs(ends) : 32; // parts of these 32
-            const float mine = lane < n ? ml.x : -INFINITY;
-            float m = mine;
+        for (int base = 0; base < n; base += 32 * wpr) { // this warp's parts: 32 at a time, sub + wpr * lane
+            const int s = base + sub + wpr * lane;
+            const float2 ml = s < n ? *reinterpret_cast<const float2*>(p.part_ml + 2 * part_row(s)) : make_float2(-INFINITY, 0.f);
+            float m = ml.x;
 #pragma unroll
             for (int sh = 16; sh > 0; sh >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, sh));
             const float m_new = fmaxf(M, m), m_ref = m_new == -INFINITY ? 0.f : m_new;
-            float l = lane < n ? ml.y * ex2_approx(mine - m_ref) : 0.f;
+            const float f = ex2_approx(ml.x - m_ref), back = ex2_approx(M - m_ref);
+            float l = ml.y * f;
 #pragma unroll
             for (int sh = 16; sh > 0; sh >>= 1) l += __shfl_xor_sync(0xffffffffu, l, sh);
-            Lsum = fmaf(Lsum, ex2_approx(M - m_ref), l);
+            Lsum = fmaf(Lsum, back, l);
             M = m_new;
-            parts += n;
-            if (ends != 0u) break;
-        }
-        parts = min(parts, p.warps - first);
-        M_use = M == -INFINITY ? 0.f : M;
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) acc[c] *= back;
+            const int here = min(32, (n - base - sub + wpr - 1) / wpr);
 #pragma unroll 8
-        for (int s = sub; s < parts; s += wpr) {
-            const int64_t pr = part_row(s);
-            const float f = ex2_approx(p.part_ml[2 * pr] - M_use);
-            if (CPL == 4) {
-                const float4 v = *reinterpret_cast<const float4*>(p.part_o + pr * DV + 4 * lane);
-                acc[0] = fmaf(v.x, f, acc[0]);
-                acc[1] = fmaf(v.y, f, acc[1]);
-                acc[CPL - 2] = fmaf(v.z, f, acc[CPL - 2]);
-                acc[CPL - 1] = fmaf(v.w, f, acc[CPL - 1]);
-            } else {
-                const float2 v = *reinterpret_cast<const float2*>(p.part_o + pr * DV + 2 * lane);
-                acc[0] = fmaf(v.x, f, acc[0]);
-                acc[1] = fmaf(v.y, f, acc[1]);
+            for (int i = 0; i < here; ++i) {
+                const float w = __shfl_sync(0xffffffffu, f, i);
+                const int64_t pr = part_row(base + sub + wpr * i);
+                float v[CPL];
+                if (CPL == 4) {
+                    const float4 x = *reinterpret_cast<const float4*>(p.part_o + pr * DV + 4 * lane);
+                    v[0] = x.x; v[1] = x.y; v[CPL - 2] = x.z; v[CPL - 1] = x.w;
+                } else {
+                    const float2 x = *reinterpret_cast<const float2*>(p.part_o + pr * DV + 2 * lane);
+                    v[0] = x.x; v[1] = x.y;
+                }
+#pragma unroll
+                for (int c = 0; c < CPL; ++c) acc[c] = fmaf(v[c], w, acc[c]);
             }
         }
     }
     if (wpr > 1) {
+        __shared__ float red_m[MERGE_WARPS], red_l[MERGE_WARPS];
 #pragma unroll
         for (int c = 0; c < CPL; ++c) red[warp][CPL * lane + c] = acc[c];
+        if (lane == 0) {
+            red_m[warp] = M;
+            red_l[warp] = Lsum;
+        }
         __syncthreads();
         if (sub == 0)
-            for (int w = 1; w < wpr; ++w)
+            for (int w = 1; w < wpr; ++w) {
+                const float m_new = fmaxf(M, red_m[warp + w]), m_ref = m_new == -INFINITY ? 0.f : m_new;
+                const float fa = ex2_approx(M - m_ref), fb = ex2_approx(red_m[warp + w] - m_ref);
+                Lsum = Lsum * fa + red_l[warp + w] * fb;
+                M = m_new;
 #pragma unroll
-                for (int c = 0; c < CPL; ++c) acc[c] += red[warp + w][CPL * lane + c];
+                for (int c = 0; c < CPL; ++c) acc[c] = acc[c] * fa + red[warp + w][CPL * lane + c] * fb;
+            }
     }
     if (!live || sub != 0) return;
+    const float M_use = M == -INFINITY ? 0.f : M;
     const int64_t orow = static_cast<int64_t>(pair_bh) * p.R + r;
     const float inv = Lsum == 0.f ? 0.f : 1.f / Lsum;
 #pragma unroll
