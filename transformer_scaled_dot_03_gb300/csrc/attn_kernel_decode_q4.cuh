@@ -323,9 +323,6 @@ attn_decode_q4_kernel(const DecodeQ4Params p)
         ok = mbar_wait(bar_never, 0, abort_word, p.status, STATUS_FORCED, 20000000ull);
         ok = __all_sync(0xffffffffu, ok);
     }
-    // one block now, the others of the ring behind the first query rows: so every warp's
-    // first block comes early
-    if (ok && ahead.todo > 0) issue();
 
     const int pi = 4 * (g & 1) + (g >> 1);               // slot of tile row g inside a 16-slot tile
     // byte offsets of this thread's codes and words inside a block
@@ -354,22 +351,31 @@ attn_decode_q4_kernel(const DecodeQ4Params p)
         uint32_t bq[NT][NGK][4][2], bz[NT][NGK];
         float ef[NT][2];                                 // raw scores to the log2 domain
         int min_lim = end;                               // every row sees the slots below it
+        uint32_t qraw[NT][NGK][8];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int r = r0 + row_of(8 * nt + g);
-            uint32_t qv[NGK][8];
-            uint32_t top = 0u;
 #pragma unroll
             for (int q = 0; q < NGK; ++q) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) qv[q][i] = 0u;
+                for (int i = 0; i < 8; ++i) qraw[nt][q][i] = 0u;
                 if (r < p.R) {
                     const uint4* qp = reinterpret_cast<const uint4*>(p.Q + (pair_bh * p.R + r) * DK + 64 * q + 16 * t);
                     const uint4 x = __ldg(qp), y = __ldg(qp + 1);
-                    qv[q][0] = x.x; qv[q][1] = x.y; qv[q][2] = x.z; qv[q][3] = x.w;
-                    qv[q][4] = y.x; qv[q][5] = y.y; qv[q][6] = y.z; qv[q][7] = y.w;
+                    qraw[nt][q][0] = x.x; qraw[nt][q][1] = x.y; qraw[nt][q][2] = x.z; qraw[nt][q][3] = x.w;
+                    qraw[nt][q][4] = y.x; qraw[nt][q][5] = y.y; qraw[nt][q][6] = y.z; qraw[nt][q][7] = y.w;
                 }
             }
+        }
+        // the worker's first copy goes out behind its first query rows (these would queue
+        // behind every worker's blocks), the others of the ring behind their conversion, so
+        // that every worker's first block comes early
+        if (issued == 0 && ahead.todo > 0) issue();
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = r0 + row_of(8 * nt + g);
+            const auto& qv = qraw[nt];
+            uint32_t top = 0u;
             {
                 // the row's mask and bias, while the loads are under way
                 const int i = r % p.n;
@@ -784,6 +790,7 @@ attn_decode_q4_kernel(const DecodeQ4Params p)
 // Merge of the parts of the cut pairs, p.merge_warps warps to each (pair, row): slot 1 of
 // worker pair_parts[pair].x, then the slots 0 of the workers after it up to pair_parts[pair].y.
 constexpr int MERGE_WARPS = 8;                           // per CTA
+constexpr int EARLY = 4;                                 // parts whose O a warp asks for at once
 
 template <int DV>
 __global__ void __launch_bounds__(32 * MERGE_WARPS)
@@ -810,9 +817,28 @@ attn_decode_q4_merge_kernel(const DecodeQ4Params p, int tile_rows)
         auto part_row = [&](int s) -> int64_t {
             return static_cast<int64_t>(s == 0 ? 2 * span.x + 1 : 2 * (span.x + s)) * p.part_rows + row;
         };
+        auto fetch = [&](float (&v)[EARLY][CPL], int base, int i, int here) {
+#pragma unroll
+            for (int j = 0; j < EARLY; ++j) {
+                const float* src = p.part_o + part_row(base + sub + wpr * (i + j)) * DV;
+                if (i + j >= here) {
+#pragma unroll
+                    for (int c = 0; c < CPL; ++c) v[j][c] = 0.f;
+                } else if (CPL == 4) {
+                    const float4 x = *reinterpret_cast<const float4*>(src + 4 * lane);
+                    v[j][0] = x.x; v[j][1] = x.y; v[j][CPL - 2] = x.z; v[j][CPL - 1] = x.w;
+                } else {
+                    const float2 x = *reinterpret_cast<const float2*>(src + 2 * lane);
+                    v[j][0] = x.x; v[j][1] = x.y;
+                }
+            }
+        };
         for (int base = 0; base < n; base += 32 * wpr) { // this warp's parts: 32 at a time, sub + wpr * lane
             const int s = base + sub + wpr * lane;
             const float2 ml = s < n ? *reinterpret_cast<const float2*>(p.part_ml + 2 * part_row(s)) : make_float2(-INFINITY, 0.f);
+            const int here = min(32, (n - base - sub + wpr - 1) / wpr);
+            float early[EARLY][CPL];                     // asked for together with the maxima
+            fetch(early, base, 0, here);
             float m = ml.x;
 #pragma unroll
             for (int sh = 16; sh > 0; sh >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, sh));
@@ -825,21 +851,23 @@ attn_decode_q4_merge_kernel(const DecodeQ4Params p, int tile_rows)
             M = m_new;
 #pragma unroll
             for (int c = 0; c < CPL; ++c) acc[c] *= back;
-            const int here = min(32, (n - base - sub + wpr - 1) / wpr);
-#pragma unroll 8
-            for (int i = 0; i < here; ++i) {
-                const float w = __shfl_sync(0xffffffffu, f, i);
-                const int64_t pr = part_row(base + sub + wpr * i);
-                float v[CPL];
-                if (CPL == 4) {
-                    const float4 x = *reinterpret_cast<const float4*>(p.part_o + pr * DV + 4 * lane);
-                    v[0] = x.x; v[1] = x.y; v[CPL - 2] = x.z; v[CPL - 1] = x.w;
+            for (int i = 0; i < here; i += EARLY) {
+                float v[EARLY][CPL];
+                if (i == 0) {
+#pragma unroll
+                    for (int j = 0; j < EARLY; ++j)
+#pragma unroll
+                        for (int c = 0; c < CPL; ++c) v[j][c] = early[j][c];
                 } else {
-                    const float2 x = *reinterpret_cast<const float2*>(p.part_o + pr * DV + 2 * lane);
-                    v[0] = x.x; v[1] = x.y;
+                    fetch(v, base, i, here);
                 }
 #pragma unroll
-                for (int c = 0; c < CPL; ++c) acc[c] = fmaf(v[c], w, acc[c]);
+                for (int j = 0; j < EARLY; ++j) {
+                    const float w = __shfl_sync(0xffffffffu, f, (i + j) & 31);
+#pragma unroll
+                    for (int c = 0; c < CPL; ++c)
+                        if (i + j < here) acc[c] = fmaf(v[j][c], w, acc[c]);
+                }
             }
         }
     }
