@@ -1040,6 +1040,7 @@ int q4_read(const void* cache, int B, int H, int H_kv, int m, int first, int n, 
     p.d_k = d_k;
     p.d_v = d_v;
     p.blocks = q4_blocks(m);
+    p.wide = aligned(K, 32) && aligned(V, 32);
     p.key_lengths = key_lengths;
     p.K = static_cast<uint16_t*>(K);
     p.V = static_cast<uint16_t*>(V);
@@ -1080,8 +1081,11 @@ extern "C" int attn_cache_q4_write(const void* K, const void* V, int B, int H_kv
     p.d_k = d_k;
     p.d_v = d_v;
     p.blocks = q4_blocks(m);
+    p.wide = aligned(K, 32) && aligned(V, 32);
     p.k_groups = static_cast<uint32_t>(rows * (d_k / attn::q4::GROUP));
     p.groups = static_cast<uint32_t>(groups);
+    p.by_n = attn::Divider(static_cast<uint32_t>(n));
+    p.by_H = attn::Divider(static_cast<uint32_t>(H_kv));
     p.starts = starts;
     p.counts = counts;
     p.cache = static_cast<uint8_t*>(cache);

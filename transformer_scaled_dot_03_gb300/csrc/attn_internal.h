@@ -139,6 +139,25 @@ struct DecodeParams {
 cudaError_t launch_decode(int d_k, int d_v, int rows, const CUtensorMap& tmK, const CUtensorMap& tmV,
                           const DecodeParams& p, cudaStream_t stream);
 
+// Division of x < 2^31 by a fixed d >= 1 as a product: q = x m >> (31 + s), 2^s >= d,
+// m = floor(2^(31 + s) / d) + 1 < 2^32 (Granlund and Montgomery, "Division by invariant
+// integers using multiplication").
+struct Divider {
+    uint32_t m, s;
+
+    explicit Divider(uint32_t d = 1) : m(0), s(0)
+    {
+        while ((1ull << s) < d) ++s;
+        m = static_cast<uint32_t>((1ull << (31 + s)) / d + 1);
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ uint32_t divide(uint32_t x) const
+    {
+        return static_cast<uint32_t>(static_cast<uint64_t>(x) * m >> (31 + s));
+    }
+#endif
+};
+
 // A key/value cache held in 4 bits (format: attn_cache_q4.cuh).
 struct CacheQ4WriteParams {
     const uint16_t* K;            // bf16 [B,H,n,d_k], H the cache's heads
@@ -147,6 +166,8 @@ struct CacheQ4WriteParams {
     int d_k, d_v;
     int blocks;                   // ceil(m / 64)
     uint32_t k_groups, groups;    // groups of 64 channels in K, and in K and V
+    bool wide;                    // K and V are 32-byte aligned
+    Divider by_n, by_H;
     const int32_t* starts;        // device int32 [B] or null (0)
     const int32_t* counts;        // device int32 [B] or null (n)
     uint8_t* cache;
@@ -158,6 +179,7 @@ struct CacheQ4ReadParams {
     int m, first, n, tiles;       // tiles = ceil(n / 64)
     int d_k, d_v;
     int blocks;
+    bool wide;                    // K and V are 32-byte aligned
     const int32_t* key_lengths;   // device int32 [B] or null (m)
     uint16_t* K;                  // bf16 [B,H,n,d_k]
     uint16_t* V;                  // bf16 [B,H,n,d_v]
