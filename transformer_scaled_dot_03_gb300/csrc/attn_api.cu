@@ -1027,11 +1027,12 @@ Q4Plan q4_plan(int64_t B, int64_t H, int64_t H_kv, int64_t n, int m, int d_k, in
 int q4_read(const void* cache, int B, int H, int H_kv, int m, int first, int n, int d_k, int d_v,
             const int32_t* key_lengths, void* K, void* V, cudaStream_t st)
 {
+    const int64_t rows = static_cast<int64_t>(B) * H_kv * n;
+    const int64_t pieces = rows <= INT32_MAX ? rows * ((d_k + d_v) / 16) : INT64_MAX;
+    if (pieces > INT32_MAX) return ATTN_ERR_UNSUPPORTED;
     attn::CacheQ4ReadParams p;
     p.cache = static_cast<const uint8_t*>(cache);
-    p.B = B;
-    p.H = H;
-    p.H_kv = H_kv;
+    p.heads = B * H_kv;
     p.group = H / H_kv;
     p.m = m;
     p.first = first;
@@ -1040,11 +1041,14 @@ int q4_read(const void* cache, int B, int H, int H_kv, int m, int first, int n, 
     p.d_k = d_k;
     p.d_v = d_v;
     p.blocks = q4_blocks(m);
+    p.k_pieces = static_cast<uint32_t>(rows * (d_k / 16));
+    p.pieces = static_cast<uint32_t>(pieces);
     p.wide = aligned(K, 32) && aligned(V, 32);
+    p.by_n = attn::Divider(static_cast<uint32_t>(n));
+    p.by_H = attn::Divider(static_cast<uint32_t>(H_kv));
     p.key_lengths = key_lengths;
     p.K = static_cast<uint16_t*>(K);
     p.V = static_cast<uint16_t*>(V);
-    if (static_cast<int64_t>(B) * H_kv * p.tiles > INT32_MAX) return ATTN_ERR_UNSUPPORTED;
     const cudaError_t e = attn::launch_cache_q4_read(p, st);
     return e == cudaSuccess ? ATTN_OK : fail_cuda("cache read kernel launch", e);
 }
@@ -1075,9 +1079,10 @@ extern "C" int attn_cache_q4_write(const void* K, const void* V, int B, int H_kv
     attn::CacheQ4WriteParams p;
     p.K = static_cast<const uint16_t*>(K);
     p.V = static_cast<const uint16_t*>(V);
-    p.H = H_kv;
+    p.heads = B * H_kv;
     p.n = n;
     p.m = m;
+    p.tiles = q4_blocks(n);
     p.d_k = d_k;
     p.d_v = d_v;
     p.blocks = q4_blocks(m);

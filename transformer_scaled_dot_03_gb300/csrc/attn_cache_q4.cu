@@ -4,6 +4,7 @@
 // the group's step, zero and addresses are then shared by 16, and loads and stores of
 // bf16 rows are 32 bytes a lane, 1 KB a warp.
 #include <cstdint>
+#include <type_traits>
 #include <cuda_runtime.h>
 
 #include "attn_cache_q4.cuh"
@@ -107,23 +108,27 @@ __device__ __forceinline__ uint2 quantise(const uint32_t (&w)[8], uint32_t* word
         u0 = __float_as_uint(rint_ratio(neg, r)) - RINT_BITS;
         // rint(x / s) + u0 is in 0..15 (rint is odd and monotone, |x| <= hi or neg), except
         // that two exact halves at the ends may add up to 16
-        const bool sixteen = __float_as_uint(rint_ratio(hi, r)) - RINT_BITS + u0 > 15u;
-        const float most = RINT + 15.f - static_cast<float>(u0);
-        uint32_t c[2];
+        // the rounded sums' bits times 16^i, modulo 2^32
+        auto encode = [&](auto&& rounded) {
+            uint32_t c[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t sum = 0u;                           // the rounded sums' bits times 16^i, modulo 2^32
+            for (int h = 0; h < 2; ++h) {
+                uint32_t sum = 0u;
 #pragma unroll
-            for (int i = 7; i >= 0; --i) {
-                const uint32_t pair = w[4 * h + i / 2];
-                const float x = __uint_as_float(i % 2 ? pair & 0xFFFF0000u : pair << 16);
-                float y = rint_ratio(x, r);
-                if (sixteen) y = fminf(y, most);
-                sum = sum * 16u + __float_as_uint(y);
+                for (int i = 7; i >= 0; --i) {
+                    const uint32_t pair = w[4 * h + i / 2];
+                    sum = sum * 16u + __float_as_uint(rounded(__uint_as_float(i % 2 ? pair & 0xFFFF0000u : pair << 16)));
+                }
+                c[h] = sum - (RINT_BITS - u0) * 0x11111111u;
             }
-            c[h] = sum - (RINT_BITS - u0) * 0x11111111u;
+            return make_uint2(c[0], c[1]);
+        };
+        if (__float_as_uint(rint_ratio(hi, r)) - RINT_BITS + u0 <= 15u) {
+            codes = encode([&](float x) { return rint_ratio(x, r); });
+        } else {
+            const float most = RINT + 15.f - static_cast<float>(u0);
+            codes = encode([&](float x) { return fminf(rint_ratio(x, r), most); });
         }
-        codes = make_uint2(c[0], c[1]);
     } else {
         sb = (__float_as_uint(__fdiv_rn(range, 15.f)) + 0xFFFFFu) & 0xFFF00000u;
         const float s = __uint_as_float(sb);
@@ -145,62 +150,124 @@ __device__ __forceinline__ uint2 quantise(const uint32_t (&w)[8], uint32_t* word
     return codes;
 }
 
-constexpr int WRITE_GROUPS = 64;                         // groups a CTA takes at once
-constexpr int WRITE_ROUNDS = 1;
+// Codes and word of one lane's quarter of group q of the slot k, into the K or V part of its block.
+template <int D, bool IS_V>
+__device__ __forceinline__ void put(uint8_t* part, int k, int q, int t, uint2 codes, uint32_t word)
+{
+    if (IS_V) {
+        *reinterpret_cast<uint32_t*>(part + q4::v_code_off(k, q, 2 * t, D)) = codes.x;
+        *reinterpret_cast<uint32_t*>(part + q4::v_code_off(k, q, 2 * t + 1, D)) = codes.y;
+    } else {
+        *reinterpret_cast<uint2*>(part + q4::k_code_off(k, q, 2 * t, D)) = codes;
+    }
+    if (t == 0) *reinterpret_cast<uint16_t*>(part + 32 * D + 2 * (k * (D / q4::GROUP) + q)) = static_cast<uint16_t>(word);
+}
 
-// Four lanes take one group of one row; the codes of a warp's eight groups fill whole
-// 32-byte sectors of the cache.
+// f(integral constant D, integral constant IS_V) for a side's head dim.
+template <bool IS_V, typename F>
+__device__ __forceinline__ void with_dim(int d, F&& f)
+{
+    if (d == 128) f(std::integral_constant<int, 128>(), std::integral_constant<bool, IS_V>());
+    else f(std::integral_constant<int, 64>(), std::integral_constant<bool, IS_V>());
+}
+
+__device__ __forceinline__ uint8_t* block_of(const CacheQ4WriteParams& p, uint32_t bh, int64_t slot)
+{
+    return p.cache + (static_cast<int64_t>(bh) * p.blocks + slot / q4::BLOCK) * q4::block_bytes(p.d_k, p.d_v);
+}
+
+// Few rows: four lanes take one group of one row, and nothing else. The codes of a
+// warp's eight groups fill whole 32-byte sectors of the cache.
 __global__ void __launch_bounds__(256) cache_q4_write_kernel(const CacheQ4WriteParams p)
 {
     griddep_wait();   // K, V and the positions of the earlier kernels are visible, their reads of the cache done
     const int t = threadIdx.x % 4;
-    uint32_t w[WRITE_ROUNDS][8];
-    uint8_t* dst[WRITE_ROUNDS];                          // codes, or null for a row that is not written
-    int slot_k[WRITE_ROUNDS];
+    const uint32_t gi = blockIdx.x * 64u + threadIdx.x / 4u;
+    const bool is_v = gi >= p.k_groups;
+    const uint32_t gj = is_v ? gi - p.k_groups : gi;
+    const int d = is_v ? p.d_v : p.d_k;
+    const uint32_t row = d == 128 ? gj >> 1 : gj;
+    const int q = d == 128 ? static_cast<int>(gj & 1u) : 0;
+    const uint32_t bh = p.by_n.divide(row);
+    const int i = static_cast<int>(row - bh * static_cast<uint32_t>(p.n));
+    uint32_t w[8];
 #pragma unroll
-    for (int u = 0; u < WRITE_ROUNDS; ++u) {
-        const uint32_t gi = (blockIdx.x * WRITE_ROUNDS + u) * WRITE_GROUPS + threadIdx.x / 4u;
-        const bool is_v = gi >= p.k_groups;
-        const uint32_t gj = is_v ? gi - p.k_groups : gi;
-        const int d = is_v ? p.d_v : p.d_k;
-        const uint32_t row = d == 128 ? gj >> 1 : gj;
-        const int q = d == 128 ? static_cast<int>(gj & 1u) : 0;
-        const uint32_t bh = p.by_n.divide(row);
-        const int i = static_cast<int>(row - bh * static_cast<uint32_t>(p.n));
+    for (int k = 0; k < 8; ++k) w[k] = 0u;
+    int64_t slot = -1;
+    if (gi < p.groups) {
         const int b = static_cast<int>(p.by_H.divide(bh));
-        dst[u] = nullptr;
-        slot_k[u] = 0;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) w[u][k] = 0u;
-        if (gi < p.groups) {
-            const int start = p.starts != nullptr ? __ldg(p.starts + b) : 0;
-            const int count = p.counts != nullptr ? __ldg(p.counts + b) : p.n;
-            const int64_t slot = static_cast<int64_t>(start) + i;
-            if (i < count && slot >= 0 && slot < p.m) {
-                load32((is_v ? p.V : p.K) + static_cast<int64_t>(row) * d + q * q4::GROUP + 16 * t, p.wide, w[u]);
-                const int k = static_cast<int>(slot) % q4::BLOCK;
-                dst[u] = p.cache + (static_cast<int64_t>(bh) * p.blocks + slot / q4::BLOCK) * q4::block_bytes(p.d_k, p.d_v) +
-                         (is_v ? q4::v_off(p.d_k) : 0);
-                slot_k[u] = (is_v ? 256 : 0) | q << 7 | k;
-            }
+        const uint16_t* src = (is_v ? p.V : p.K) + static_cast<int64_t>(row) * d + q * q4::GROUP + 16 * t;
+        // (without counts the row is read at once, not behind the positions)
+        if (p.counts == nullptr || i < __ldg(p.counts + b)) {
+            load32(src, p.wide, w);
+            slot = static_cast<int64_t>(p.starts != nullptr ? __ldg(p.starts + b) : 0) + i;
         }
     }
+    uint32_t word;
+    const uint2 codes = quantise(w, &word);
+    if (slot < 0 || slot >= p.m) return;
+    uint8_t* blk = block_of(p, bh, slot);
+    const int k = static_cast<int>(slot) % q4::BLOCK;
+    if (is_v) with_dim<true>(d, [&](auto D, auto S) { put<D(), S()>(blk + q4::v_off(p.d_k), k, q, t, codes, word); });
+    else with_dim<false>(d, [&](auto D, auto S) { put<D(), S()>(blk, k, q, t, codes, word); });
+}
+
+constexpr int TILE = 64;                                 // rows of a CTA
+
+// Many rows: a CTA takes 64 rows of one (b, cache head), K and V, into shared memory
+// with asynchronous copies (32 KB in flight, whatever the registers hold), and
+// quantises them from there.
+__global__ void __launch_bounds__(256) cache_q4_write_tile_kernel(const CacheQ4WriteParams p)
+{
+    extern __shared__ __align__(128) uint8_t smem[];
+    griddep_wait();   // K, V and the positions of the earlier kernels are visible, their reads of the cache done
+    const uint32_t bh = blockIdx.x / static_cast<uint32_t>(p.tiles);
+    const int i0 = static_cast<int>(blockIdx.x - bh * static_cast<uint32_t>(p.tiles)) * TILE;
+    const int b = static_cast<int>(p.by_H.divide(bh));
+    const int64_t start = p.starts != nullptr ? __ldg(p.starts + b) : 0;
+    const int count = min(p.n, p.counts != nullptr ? __ldg(p.counts + b) : p.n);
+    // rows [lo, hi) of the tile have a slot
+    const int lo = static_cast<int>(min(static_cast<int64_t>(TILE), max(static_cast<int64_t>(0), -start - i0)));
+    const int hi = static_cast<int>(min(static_cast<int64_t>(TILE), min(static_cast<int64_t>(count), p.m - start) - i0));
+    if (lo >= hi) return;
+    const int rows = hi - lo;
+    const int v_at = TILE * p.d_k * 2;                   // V's rows in shared memory
+    const uint32_t sbase = smem_u32(smem);
 #pragma unroll
-    for (int u = 0; u < WRITE_ROUNDS; ++u) {
-        uint32_t word;
-        const uint2 codes = quantise(w[u], &word);
-        if (dst[u] == nullptr) continue;
-        const bool is_v = slot_k[u] & 256;
-        const int q = slot_k[u] >> 7 & 1, k = slot_k[u] & 127;
-        const int d = is_v ? p.d_v : p.d_k;
-        if (is_v) {
-            *reinterpret_cast<uint32_t*>(dst[u] + q4::v_code_off(k, q, 2 * t, d)) = codes.x;
-            *reinterpret_cast<uint32_t*>(dst[u] + q4::v_code_off(k, q, 2 * t + 1, d)) = codes.y;
-        } else {
-            *reinterpret_cast<uint2*>(dst[u] + q4::k_code_off(k, q, 2 * t, d)) = codes;
-        }
-        if (t == 0) *reinterpret_cast<uint16_t*>(dst[u] + 32 * d + 2 * (k * (d / q4::GROUP) + q)) = static_cast<uint16_t>(word);
+    for (int side = 0; side < 2; ++side) {
+        const int d = side ? p.d_v : p.d_k;
+        const uint8_t* src = reinterpret_cast<const uint8_t*>(side ? p.V : p.K) +
+                             ((static_cast<int64_t>(bh) * p.n + i0 + lo) * d) * 2;
+        for (int e = threadIdx.x; e < rows * d / 8; e += 256)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sbase + (side ? v_at : 0) + 16 * e), "l"(src + 16 * e)
+                         : "memory");
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    const int t = threadIdx.x % 4;
+    const int64_t slot0 = start + i0 + lo;
+    uint8_t* blk0 = block_of(p, bh, slot0);
+    const int k0 = static_cast<int>(slot0 % q4::BLOCK);  // the rows' slots lie in this block and the next
+    auto side = [&](auto D, auto S) {
+        constexpr int d = D(), ng = d / q4::GROUP;
+        const uint8_t* src0 = smem + (S() ? v_at : 0);
+        uint8_t* part0 = blk0 + (S() ? q4::v_off(p.d_k) : 0);
+        for (int g0 = 0; g0 < rows * ng; g0 += 64) {     // (whole warps: the quantiser's lanes exchange maxima)
+            const int gi = g0 + static_cast<int>(threadIdx.x / 4u);
+            const bool live = gi < rows * ng;
+            const int r = live ? gi / ng : 0, q = gi % ng;
+            const uint4* src = reinterpret_cast<const uint4*>(src0 + (r * d + q * q4::GROUP + 16 * t) * 2);
+            const uint4 a = src[0], c = src[1];
+            const uint32_t w[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+            uint32_t word;
+            const uint2 codes = quantise(w, &word);
+            const int k = k0 + r;
+            if (live)
+                put<d, S()>(part0 + (k >= q4::BLOCK ? q4::block_bytes(p.d_k, p.d_v) : 0), k % q4::BLOCK, q, t, codes, word);
+        }
+    };
+    with_dim<false>(p.d_k, side);
+    with_dim<true>(p.d_v, side);
 }
 
 // Values of 16 codes, s (u - u0), in packed bf16: 128 + u and 128 + u0 have eight bits, so
@@ -225,74 +292,144 @@ __device__ __forceinline__ void values(uint2 codes, uint32_t word, uint32_t (&ou
     }
 }
 
-constexpr int READ_ROUNDS = 1;                           // 16-channel pieces a lane has in flight
+// A 16-channel piece to read: its codes and word, and its place in the output (null: none).
+struct ReadItem {
+    uint2 codes;
+    uint32_t word;
+    uint16_t* dst;
+    int64_t head;                                        // elements from a query head's copy to the next
+};
 
-// One CTA per (b, cache head, 64 slots): the slots' K and V as bf16 for each of the
-// query heads that share them. Slots at or past the entry's length give 0.
+__device__ __forceinline__ ReadItem fetch(const CacheQ4ReadParams& p, uint32_t e)
+{
+    ReadItem x;
+    x.codes = make_uint2(0u, 0u);
+    x.word = 0u;
+    x.dst = nullptr;
+    x.head = 0;
+    if (e >= p.pieces) return x;
+    const bool is_v = e >= p.k_pieces;
+    const uint32_t ee = is_v ? e - p.k_pieces : e;
+    const int d = is_v ? p.d_v : p.d_k;
+    const uint32_t row = d == 128 ? ee >> 3 : ee >> 2;
+    const int piece = static_cast<int>(ee) & (d / 16 - 1), q = piece >> 2, t = piece & 3;
+    const uint32_t bh = p.by_n.divide(row);
+    const int j = static_cast<int>(row - bh * static_cast<uint32_t>(p.n));
+    const uint32_t b = p.by_H.divide(bh);
+    const int slot = p.first + j;
+    const int len = p.key_lengths != nullptr ? __ldg(p.key_lengths + b) : p.m;
+    x.head = static_cast<int64_t>(p.n) * d;
+    x.dst = (is_v ? p.V : p.K) + static_cast<int64_t>(bh) * p.group * x.head + static_cast<int64_t>(j) * d + 16 * piece;
+    if (slot < len) {
+        const int k = slot % q4::BLOCK;
+        const uint8_t* blk = p.cache + (static_cast<int64_t>(bh) * p.blocks + slot / q4::BLOCK) * q4::block_bytes(p.d_k, p.d_v) +
+                             (is_v ? q4::v_off(p.d_k) : 0);
+        if (is_v) {
+            x.codes.x = __ldg(reinterpret_cast<const uint32_t*>(blk + q4::v_code_off(k, q, 2 * t, d)));
+            x.codes.y = __ldg(reinterpret_cast<const uint32_t*>(blk + q4::v_code_off(k, q, 2 * t + 1, d)));
+        } else {
+            x.codes = __ldg(reinterpret_cast<const uint2*>(blk + q4::k_code_off(k, q, 2 * t, d)));
+        }
+        x.word = __ldg(reinterpret_cast<const uint16_t*>(blk + 32 * d) + k * (d / q4::GROUP) + q);
+    }
+    return x;
+}
+
+// Little to read: a piece per lane. The slots' K and V as bf16 for each of the query
+// heads that share a cache head; slots at or past the entry's length give 0.
 __global__ void __launch_bounds__(256) cache_q4_read_kernel(const CacheQ4ReadParams p)
 {
     griddep_wait();   // the earlier kernels' writes into the cache are visible, their reads of K and V done
-    const uint32_t tiles = static_cast<uint32_t>(p.tiles);
-    const uint32_t bh = blockIdx.x / tiles;
-    const int j0 = static_cast<int>(blockIdx.x - bh * tiles) * q4::BLOCK;      // first output row
-    const int b = static_cast<int>(bh / static_cast<uint32_t>(p.H_kv));
-    const int hk = static_cast<int>(bh - static_cast<uint32_t>(b) * p.H_kv);
+    const ReadItem x = fetch(p, blockIdx.x * 256u + threadIdx.x);
+    if (x.dst == nullptr) return;
+    uint32_t out[8];
+    values(x.codes, x.word, out);
+    for (int g = 0; g < p.group; ++g) store32(x.dst + g * x.head, p.wide, out);
+}
+
+// Much to read: a CTA takes 64 slots of one (b, cache head), puts their K and V into
+// shared memory as they lie in the output (one contiguous run each), and bulk stores
+// write the runs.
+__global__ void __launch_bounds__(256) cache_q4_read_tile_kernel(const CacheQ4ReadParams p)
+{
+    extern __shared__ __align__(128) uint8_t smem[];
+    griddep_wait();   // the earlier kernels' writes into the cache are visible, their reads of K and V done
+    const uint32_t bh = blockIdx.x / static_cast<uint32_t>(p.tiles);
+    const int j0 = static_cast<int>(blockIdx.x - bh * static_cast<uint32_t>(p.tiles)) * TILE;
+    const int b = static_cast<int>(p.by_H.divide(bh));
     const int len = p.key_lengths != nullptr ? __ldg(p.key_lengths + b) : p.m;
+    const int rows = min(TILE, p.n - j0);
+    const int v_at = TILE * p.d_k * 2;
     const uint8_t* base = p.cache + static_cast<int64_t>(bh) * p.blocks * q4::block_bytes(p.d_k, p.d_v);
-    const int rows = min(q4::BLOCK, p.n - j0);
-    const int64_t head0 = (static_cast<int64_t>(b) * p.H + static_cast<int64_t>(hk) * p.group);
-    const int k_pieces = rows * (p.d_k / 16), pieces = k_pieces + rows * (p.d_v / 16);
-    for (int e0 = threadIdx.x; e0 < pieces; e0 += 256 * READ_ROUNDS) {
-        uint2 codes[READ_ROUNDS];
-        uint32_t word[READ_ROUNDS];
-        uint16_t* dst[READ_ROUNDS];
-#pragma unroll
-        for (int u = 0; u < READ_ROUNDS; ++u) {
-            const int e = e0 + 256 * u;
-            const bool is_v = e >= k_pieces;
-            const int ee = is_v ? e - k_pieces : e;
-            const int d = is_v ? p.d_v : p.d_k;
-            const int r = d == 128 ? ee >> 3 : ee >> 2;
-            const int piece = ee & (d / 16 - 1), q = piece >> 2, t = piece & 3;
+    auto side = [&](auto D, auto S) {
+        constexpr int d = D();
+        const int pieces = rows * (d / 16);
+#pragma unroll 2
+        for (int e = threadIdx.x; e < pieces; e += 256) {
+            const int r = e / (d / 16), piece = e % (d / 16), q = piece >> 2, t = piece & 3;
             const int slot = p.first + j0 + r;
-            codes[u] = make_uint2(0u, 0u);
-            word[u] = 0u;
-            dst[u] = e < pieces ? (is_v ? p.V : p.K) + (head0 * p.n + j0 + r) * d + 16 * piece : nullptr;
-            if (e < pieces && slot < len) {
+            uint2 codes = make_uint2(0u, 0u);
+            uint32_t word = 0u;
+            if (slot < len) {
                 const int k = slot % q4::BLOCK;
-                const uint8_t* blk = base + static_cast<int64_t>(slot / q4::BLOCK) * q4::block_bytes(p.d_k, p.d_v) +
-                                     (is_v ? q4::v_off(p.d_k) : 0);
-                if (is_v) {
-                    codes[u].x = __ldg(reinterpret_cast<const uint32_t*>(blk + q4::v_code_off(k, q, 2 * t, d)));
-                    codes[u].y = __ldg(reinterpret_cast<const uint32_t*>(blk + q4::v_code_off(k, q, 2 * t + 1, d)));
+                const uint8_t* part = base + static_cast<int64_t>(slot / q4::BLOCK) * q4::block_bytes(p.d_k, p.d_v) +
+                                      (S() ? q4::v_off(p.d_k) : 0);
+                if (S()) {
+                    codes.x = __ldg(reinterpret_cast<const uint32_t*>(part + q4::v_code_off(k, q, 2 * t, d)));
+                    codes.y = __ldg(reinterpret_cast<const uint32_t*>(part + q4::v_code_off(k, q, 2 * t + 1, d)));
                 } else {
-                    codes[u] = __ldg(reinterpret_cast<const uint2*>(blk + q4::k_code_off(k, q, 2 * t, d)));
+                    codes = __ldg(reinterpret_cast<const uint2*>(part + q4::k_code_off(k, q, 2 * t, d)));
                 }
-                word[u] = __ldg(reinterpret_cast<const uint16_t*>(blk + 32 * d) + k * (d / q4::GROUP) + q);
+                word = __ldg(reinterpret_cast<const uint16_t*>(part + 32 * d) + k * (d / q4::GROUP) + q);
             }
-        }
-#pragma unroll
-        for (int u = 0; u < READ_ROUNDS; ++u) {
-            if (dst[u] == nullptr) continue;
             uint32_t out[8];
-            values(codes[u], word[u], out);
-            const int64_t head = static_cast<int64_t>(p.n) * (e0 + 256 * u >= k_pieces ? p.d_v : p.d_k);
-            for (int g = 0; g < p.group; ++g) store32(dst[u] + g * head, p.wide, out);
+            values(codes, word, out);
+            uint4* dst = reinterpret_cast<uint4*>(smem + (S() ? v_at : 0) + 32 * e);
+            dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
+            dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
         }
+    };
+    with_dim<false>(p.d_k, side);
+    with_dim<true>(p.d_v, side);
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const int64_t row = static_cast<int64_t>(bh) * p.n + j0;
+        bulk_store(p.K + row * p.d_k, smem_u32(smem), static_cast<uint32_t>(rows * p.d_k * 2));
+        bulk_store(p.V + row * p.d_v, smem_u32(smem) + v_at, static_cast<uint32_t>(rows * p.d_v * 2));
+        bulk_commit_group();
+        bulk_wait_group_read0();                         // (the CTA's shared memory may go)
     }
 }
 
+// From this many rows (of one (b, cache head) and slot or token) on the tile kernels run: 16 x 8
+// heads of up to 1000 new rows written in 12.9 against 17.8 us and their 2048 slots read in
+// 23.7 against 26.6; one head's 777 slots of a batch of five read in 2.7 us by the simple
+// kernel, 3.2 by a tile kernel. Copies for several query heads go out as fast from
+// the simple kernel's registers (4 x 8192 slots for 16 heads: 42.7 us, 45.7 by tiles).
+constexpr int64_t TILE_ROWS = 152 * 8 * 16;
+
 }  // namespace
+
+template <typename Params>
+static cudaError_t launch_tiles(void (*kern)(const Params), const Params& p, uint32_t ctas, cudaStream_t stream)
+{
+    // 32 KB at most: within what every kernel may use without asking
+    return launch_pdl(kern, dim3(ctas), dim3(256), static_cast<size_t>(TILE) * (p.d_k + p.d_v) * 2, stream, p);
+}
 
 cudaError_t launch_cache_q4_write(const CacheQ4WriteParams& p, cudaStream_t stream)
 {
-    const uint32_t per = WRITE_GROUPS * WRITE_ROUNDS;
-    return launch_pdl(cache_q4_write_kernel, dim3((p.groups + per - 1) / per), dim3(256), 0, stream, p);
+    if (p.n >= TILE / 2 && static_cast<int64_t>(p.heads) * p.n >= TILE_ROWS)
+        return launch_tiles(cache_q4_write_tile_kernel, p, static_cast<uint32_t>(p.heads) * p.tiles, stream);
+    return launch_pdl(cache_q4_write_kernel, dim3((p.groups + 63u) / 64u), dim3(256), 0, stream, p);
 }
 
 cudaError_t launch_cache_q4_read(const CacheQ4ReadParams& p, cudaStream_t stream)
 {
-    return launch_pdl(cache_q4_read_kernel, dim3(static_cast<unsigned>(p.B) * p.H_kv * p.tiles), dim3(256), 0, stream, p);
+    if (p.group == 1 && p.n >= TILE / 2 && static_cast<int64_t>(p.heads) * p.n >= TILE_ROWS)
+        return launch_tiles(cache_q4_read_tile_kernel, p, static_cast<uint32_t>(p.heads) * p.tiles, stream);
+    return launch_pdl(cache_q4_read_kernel, dim3((p.pieces + 255u) / 256u), dim3(256), 0, stream, p);
 }
 
 }  // namespace attn

@@ -162,7 +162,8 @@ struct Divider {
 struct CacheQ4WriteParams {
     const uint16_t* K;            // bf16 [B,H,n,d_k], H the cache's heads
     const uint16_t* V;            // bf16 [B,H,n,d_v]
-    int H, n, m;
+    int heads;                    // B * H
+    int n, m, tiles;              // tiles = ceil(n / 64)
     int d_k, d_v;
     int blocks;                   // ceil(m / 64)
     uint32_t k_groups, groups;    // groups of 64 channels in K, and in K and V
@@ -175,11 +176,14 @@ struct CacheQ4WriteParams {
 
 struct CacheQ4ReadParams {
     const uint8_t* cache;
-    int B, H, H_kv, group;        // group = H / H_kv
+    int heads;                    // B * cache heads
+    int group;                    // query heads per cache head
     int m, first, n, tiles;       // tiles = ceil(n / 64)
     int d_k, d_v;
     int blocks;
+    uint32_t k_pieces, pieces;    // 16-channel pieces of K, and of K and V, per cache head
     bool wide;                    // K and V are 32-byte aligned
+    Divider by_n, by_H;           // by n, by the cache's heads
     const int32_t* key_lengths;   // device int32 [B] or null (m)
     uint16_t* K;                  // bf16 [B,H,n,d_k]
     uint16_t* V;                  // bf16 [B,H,n,d_v]
