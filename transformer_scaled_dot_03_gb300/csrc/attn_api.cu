@@ -204,10 +204,11 @@ int fill_no_keys(int64_t bh, int n, int d_v, void* O, float* LSE, cudaStream_t s
 
 // Tensor maps, parameters and the launch of the attention kernel (m >= 1),
 // with `status` as the kernel's device status word; `slopes` (device fp32 [H])
-// selects the kernel with the linear distance bias, null the plain one.
+// selects the kernel with the linear distance bias, null the plain one. K and V have
+// H / kv_group heads, each shared by kv_group query heads.
 int launch_attention(const void* Q, const void* K, const void* V, int B, int H, int n, int m, int d_k,
                      int d_v, int mask_kind, const int32_t* key_lengths, float scale, void* O, float* LSE,
-                     uint32_t* status, cudaStream_t st, const float* slopes = nullptr)
+                     uint32_t* status, cudaStream_t st, const float* slopes = nullptr, int kv_group = 1)
 {
     const int64_t bh = static_cast<int64_t>(B) * H;
     const int64_t num_qblocks = (static_cast<int64_t>(n) + 127) / 128;
@@ -217,13 +218,17 @@ int launch_attention(const void* Q, const void* K, const void* V, int B, int H, 
     if (rc != ATTN_OK) return rc;
     attn::TensorMaps maps;
     if ((rc = make_map(enc, &maps.q, Q, bh, n, d_k, 128)) != ATTN_OK) return rc;
-    if ((rc = make_map(enc, &maps.k, K, bh, m, d_k, 128)) != ATTN_OK) return rc;
-    if ((rc = make_map(enc, &maps.v, V, bh, m, d_v, 128)) != ATTN_OK) return rc;
+    if ((rc = make_map(enc, &maps.k, K, bh / kv_group, m, d_k, 128)) != ATTN_OK) return rc;
+    if ((rc = make_map(enc, &maps.v, V, bh / kv_group, m, d_v, 128)) != ATTN_OK) return rc;
     if ((rc = make_map(enc, &maps.o, O, bh, n, d_v, 32)) != ATTN_OK) return rc;
 
     const double sc = (scale > 0.f && std::isfinite(scale)) ? static_cast<double>(scale)
                                                              : 1.0 / std::sqrt(static_cast<double>(d_k));
-    const bool paired = attn::mask_is_causal(mask_kind);   // causal units pair two query tiles
+    int num_sms = 0;
+    if ((rc = sm_count(&num_sms)) != ATTN_OK) return rc;
+    const int64_t slots = static_cast<int64_t>(num_sms) * (d_k == 64 && d_v == 64 ? 2 : 1);
+    // causal units pair two query tiles, where there are pairs for every CTA
+    const bool paired = attn::mask_is_causal(mask_kind) && bh * ((num_qblocks + 1) / 2) >= slots;
     attn::FwdParams p;
     p.B = B;
     p.H = H;
@@ -232,6 +237,8 @@ int launch_attention(const void* Q, const void* K, const void* V, int B, int H, 
     p.causal_off = m - n;
     p.num_qblocks = static_cast<int>(num_qblocks);
     p.num_units = static_cast<int>(bh * (paired ? (num_qblocks + 1) / 2 : num_qblocks));
+    p.paired = paired ? 1 : 0;
+    p.kv_group = attn::Divider(static_cast<uint32_t>(kv_group));
     p.O = O;
     p.key_lengths = attn::mask_has_lengths(mask_kind) ? key_lengths : nullptr;
     p.scale_log2 = static_cast<float>(sc * 1.4426950408889634074);
@@ -241,8 +248,6 @@ int launch_attention(const void* Q, const void* K, const void* V, int B, int H, 
     p.watchdog_ns = g_watchdog_ns;
     p.debug_flags = g_debug_flags;
 
-    int num_sms = 0;
-    if ((rc = sm_count(&num_sms)) != ATTN_OK) return rc;
     cudaError_t e;
     if (slopes != nullptr)
         e = attn::launch_fwd_alibi(d_k, d_v, mask_kind, maps, p, num_sms, st);
@@ -1004,8 +1009,8 @@ Q4Plan q4_plan(int64_t B, int64_t H, int64_t H_kv, int64_t n, int m, int d_k, in
     const int64_t R = H / H_kv * n;
     w.few = R <= kQ4MaxRows;
     if (!w.few) {
-        w.v_off = round_up(static_cast<size_t>(B * H) * m * d_k * 2, kWsAlign);
-        w.total = w.v_off + round_up(static_cast<size_t>(B * H) * m * d_v * 2, kWsAlign);
+        w.v_off = round_up(static_cast<size_t>(B * H_kv) * m * d_k * 2, kWsAlign);
+        w.total = w.v_off + round_up(static_cast<size_t>(B * H_kv) * m * d_v * 2, kWsAlign);
         return w;
     }
     const int tile = attn::decode_q4_tile_rows(static_cast<int>(R));
@@ -1025,7 +1030,7 @@ Q4Plan q4_plan(int64_t B, int64_t H, int64_t H_kv, int64_t n, int m, int d_k, in
 }
 
 int q4_read(const void* cache, int B, int H, int H_kv, int m, int first, int n, int d_k, int d_v,
-            const int32_t* key_lengths, void* K, void* V, cudaStream_t st)
+            const int32_t* key_lengths, void* K, void* V, cudaStream_t st, bool to_tiles = false)
 {
     const int64_t rows = static_cast<int64_t>(B) * H_kv * n;
     const int64_t pieces = rows <= INT32_MAX ? rows * ((d_k + d_v) / 16) : INT64_MAX;
@@ -1044,6 +1049,7 @@ int q4_read(const void* cache, int B, int H, int H_kv, int m, int first, int n, 
     p.k_pieces = static_cast<uint32_t>(rows * (d_k / 16));
     p.pieces = static_cast<uint32_t>(pieces);
     p.wide = aligned(K, 32) && aligned(V, 32);
+    p.to_tiles = to_tiles;
     p.by_n = attn::Divider(static_cast<uint32_t>(n));
     p.by_H = attn::Divider(static_cast<uint32_t>(H_kv));
     p.key_lengths = key_lengths;
@@ -1150,11 +1156,11 @@ extern "C" int attn_decode_q4(const void* Q, const void* cache, int B, int H, in
     const int32_t* lens = attn::mask_has_lengths(mask_kind) ? key_lengths : nullptr;
 
     if (!w.few) {
-        // many rows: the cache as bf16, then the tensor-core forward
-        rc = q4_read(cache, B, H, H_kv, m, 0, m, d_k, d_v, lens, wsb, wsb + w.v_off, st);
+        // many rows: the cache as bf16 (as far as the forward's 128-key tiles go), then the tensor-core forward
+        rc = q4_read(cache, B, H_kv, H_kv, m, 0, m, d_k, d_v, lens, wsb, wsb + w.v_off, st, true);
         if (rc != ATTN_OK) return rc;
         return launch_attention(Q, wsb, wsb + w.v_off, B, H, n, m, d_k, d_v, mask_kind, lens, scale, O, LSE, status, st,
-                                slopes);
+                                slopes, H / H_kv);
     }
 
     const double sc = (scale > 0.f && std::isfinite(scale)) ? static_cast<double>(scale)

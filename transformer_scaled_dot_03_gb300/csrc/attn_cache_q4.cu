@@ -318,6 +318,7 @@ __device__ __forceinline__ ReadItem fetch(const CacheQ4ReadParams& p, uint32_t e
     const uint32_t b = p.by_H.divide(bh);
     const int slot = p.first + j;
     const int len = p.key_lengths != nullptr ? __ldg(p.key_lengths + b) : p.m;
+    if (p.to_tiles && j >= (static_cast<int64_t>(len) + 127) / 128 * 128) return x;
     x.head = static_cast<int64_t>(p.n) * d;
     x.dst = (is_v ? p.V : p.K) + static_cast<int64_t>(bh) * p.group * x.head + static_cast<int64_t>(j) * d + 16 * piece;
     if (slot < len) {
@@ -358,6 +359,7 @@ __global__ void __launch_bounds__(256) cache_q4_read_tile_kernel(const CacheQ4Re
     const int j0 = static_cast<int>(blockIdx.x - bh * static_cast<uint32_t>(p.tiles)) * TILE;
     const int b = static_cast<int>(p.by_H.divide(bh));
     const int len = p.key_lengths != nullptr ? __ldg(p.key_lengths + b) : p.m;
+    if (p.to_tiles && j0 >= (static_cast<int64_t>(len) + 127) / 128 * 128) return;
     const int rows = min(TILE, p.n - j0);
     const int v_at = TILE * p.d_k * 2;
     const uint8_t* base = p.cache + static_cast<int64_t>(bh) * p.blocks * q4::block_bytes(p.d_k, p.d_v);

@@ -36,11 +36,32 @@ enum : uint32_t {
 
 enum : uint32_t { DEBUG_FORCE_TIMEOUT = 1u };
 
+// Division of x < 2^31 by a fixed d >= 1 as a product: q = x m >> (31 + s), 2^s >= d,
+// m = floor(2^(31 + s) / d) + 1 < 2^32 (Granlund and Montgomery, "Division by invariant
+// integers using multiplication").
+struct Divider {
+    uint32_t m, s;
+
+    explicit Divider(uint32_t d = 1) : m(0), s(0)
+    {
+        while ((1ull << s) < d) ++s;
+        m = static_cast<uint32_t>((1ull << (31 + s)) / d + 1);
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ uint32_t divide(uint32_t x) const
+    {
+        return static_cast<uint32_t>(static_cast<uint64_t>(x) * m >> (31 + s));
+    }
+#endif
+};
+
 struct FwdParams {
     int B, H, n, m;
     int causal_off;               // m - n: query row i sees keys j <= i + causal_off (causal masks)
     int num_qblocks;              // ceil(n / rows per work unit)
-    int num_units;                // work units (query tiles, paired under the causal masks)
+    int num_units;                // work units (query tiles, or pairs of them)
+    int paired;                   // a unit pairs query tiles k and num_qblocks - 1 - k (causal masks, enough units)
+    Divider kv_group;             // by the query heads that share a head of K and V
     void* O;                      // bf16 [B,H,n,d_v] (persistent kernel stores rows directly)
     const int32_t* key_lengths;   // device int32 [B] (key-padding masks only)
     float scale_log2;             // scale * log2(e)
@@ -139,25 +160,6 @@ struct DecodeParams {
 cudaError_t launch_decode(int d_k, int d_v, int rows, const CUtensorMap& tmK, const CUtensorMap& tmV,
                           const DecodeParams& p, cudaStream_t stream);
 
-// Division of x < 2^31 by a fixed d >= 1 as a product: q = x m >> (31 + s), 2^s >= d,
-// m = floor(2^(31 + s) / d) + 1 < 2^32 (Granlund and Montgomery, "Division by invariant
-// integers using multiplication").
-struct Divider {
-    uint32_t m, s;
-
-    explicit Divider(uint32_t d = 1) : m(0), s(0)
-    {
-        while ((1ull << s) < d) ++s;
-        m = static_cast<uint32_t>((1ull << (31 + s)) / d + 1);
-    }
-#ifdef __CUDACC__
-    __device__ __forceinline__ uint32_t divide(uint32_t x) const
-    {
-        return static_cast<uint32_t>(static_cast<uint64_t>(x) * m >> (31 + s));
-    }
-#endif
-};
-
 // A key/value cache held in 4 bits (format: attn_cache_q4.cuh).
 struct CacheQ4WriteParams {
     const uint16_t* K;            // bf16 [B,H,n,d_k], H the cache's heads
@@ -183,6 +185,7 @@ struct CacheQ4ReadParams {
     int blocks;
     uint32_t k_pieces, pieces;    // 16-channel pieces of K, and of K and V, per cache head
     bool wide;                    // K and V are 32-byte aligned
+    bool to_tiles;                // rows past the 128-row tile that holds the last live slot are left as they are
     Divider by_n, by_H;           // by n, by the cache's heads
     const int32_t* key_lengths;   // device int32 [B] or null (m)
     uint16_t* K;                  // bf16 [B,H,n,d_k]
