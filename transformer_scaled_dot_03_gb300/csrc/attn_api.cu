@@ -204,11 +204,11 @@ int fill_no_keys(int64_t bh, int n, int d_v, void* O, float* LSE, cudaStream_t s
 
 // Tensor maps, parameters and the launch of the attention kernel (m >= 1),
 // with `status` as the kernel's device status word; `slopes` (device fp32 [H])
-// selects the kernel with the linear distance bias, null the plain one. K and V have
-// H / kv_group heads, each shared by kv_group query heads.
+// selects the kernel with the linear distance bias, null the plain one. kv_group > 0: K and V
+// have H / kv_group heads, each shared by kv_group query heads (launch_fwd_shared).
 int launch_attention(const void* Q, const void* K, const void* V, int B, int H, int n, int m, int d_k,
                      int d_v, int mask_kind, const int32_t* key_lengths, float scale, void* O, float* LSE,
-                     uint32_t* status, cudaStream_t st, const float* slopes = nullptr, int kv_group = 1)
+                     uint32_t* status, cudaStream_t st, const float* slopes = nullptr, int kv_group = 0)
 {
     const int64_t bh = static_cast<int64_t>(B) * H;
     const int64_t num_qblocks = (static_cast<int64_t>(n) + 127) / 128;
@@ -218,17 +218,15 @@ int launch_attention(const void* Q, const void* K, const void* V, int B, int H, 
     if (rc != ATTN_OK) return rc;
     attn::TensorMaps maps;
     if ((rc = make_map(enc, &maps.q, Q, bh, n, d_k, 128)) != ATTN_OK) return rc;
-    if ((rc = make_map(enc, &maps.k, K, bh / kv_group, m, d_k, 128)) != ATTN_OK) return rc;
-    if ((rc = make_map(enc, &maps.v, V, bh / kv_group, m, d_v, 128)) != ATTN_OK) return rc;
+    const int64_t kv_bh = kv_group > 0 ? bh / kv_group : bh;
+    if ((rc = make_map(enc, &maps.k, K, kv_bh, m, d_k, 128)) != ATTN_OK) return rc;
+    if ((rc = make_map(enc, &maps.v, V, kv_bh, m, d_v, 128)) != ATTN_OK) return rc;
     if ((rc = make_map(enc, &maps.o, O, bh, n, d_v, 32)) != ATTN_OK) return rc;
 
     const double sc = (scale > 0.f && std::isfinite(scale)) ? static_cast<double>(scale)
                                                              : 1.0 / std::sqrt(static_cast<double>(d_k));
-    int num_sms = 0;
-    if ((rc = sm_count(&num_sms)) != ATTN_OK) return rc;
-    const int64_t slots = static_cast<int64_t>(num_sms) * (d_k == 64 && d_v == 64 ? 2 : 1);
-    // causal units pair two query tiles, where there are pairs for every CTA
-    const bool paired = attn::mask_is_causal(mask_kind) && bh * ((num_qblocks + 1) / 2) >= slots;
+    // causal units pair two query tiles (not in the kernel for shared heads)
+    const bool paired = attn::mask_is_causal(mask_kind) && kv_group == 0;
     attn::FwdParams p;
     p.B = B;
     p.H = H;
@@ -237,8 +235,7 @@ int launch_attention(const void* Q, const void* K, const void* V, int B, int H, 
     p.causal_off = m - n;
     p.num_qblocks = static_cast<int>(num_qblocks);
     p.num_units = static_cast<int>(bh * (paired ? (num_qblocks + 1) / 2 : num_qblocks));
-    p.paired = paired ? 1 : 0;
-    p.kv_group = attn::Divider(static_cast<uint32_t>(kv_group));
+    p.kv_group = kv_group;
     p.O = O;
     p.key_lengths = attn::mask_has_lengths(mask_kind) ? key_lengths : nullptr;
     p.scale_log2 = static_cast<float>(sc * 1.4426950408889634074);
@@ -248,8 +245,13 @@ int launch_attention(const void* Q, const void* K, const void* V, int B, int H, 
     p.watchdog_ns = g_watchdog_ns;
     p.debug_flags = g_debug_flags;
 
+    int num_sms = 0;
+    if ((rc = sm_count(&num_sms)) != ATTN_OK) return rc;
     cudaError_t e;
-    if (slopes != nullptr)
+    if (kv_group > 0)
+        e = slopes != nullptr ? attn::launch_fwd_shared_alibi(d_k, d_v, mask_kind, maps, p, num_sms, st)
+                              : attn::launch_fwd_shared(d_k, d_v, mask_kind, maps, p, num_sms, st);
+    else if (slopes != nullptr)
         e = attn::launch_fwd_alibi(d_k, d_v, mask_kind, maps, p, num_sms, st);
     else if (d_k != d_v)
         e = attn::launch_fwd_dmix(d_k, d_v, mask_kind, maps, p, num_sms, st);

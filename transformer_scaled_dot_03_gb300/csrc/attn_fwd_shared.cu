@@ -1,0 +1,31 @@
+// attn_fwd_shared.cu -- instantiations of the persistent attention forward kernel for K
+// and V whose heads groups of query heads share, for head dims 64 and
+// 128 (d_k != d_v included).
+#include "attn_kernel_dp.cuh"
+
+namespace attn {
+
+template <int DK, int DV>
+static cudaError_t launch_mask(int mask, const TensorMaps& maps, const FwdParams& p, int num_sms, cudaStream_t stream)
+{
+    switch (mask) {
+    case MASK_NONE: return dp::launch<DK, DV, MASK_NONE, false, true>(maps, p, num_sms, stream);
+    case MASK_CAUSAL: return dp::launch<DK, DV, MASK_CAUSAL, false, true>(maps, p, num_sms, stream);
+    case MASK_KEY_PADDING: return dp::launch<DK, DV, MASK_KEY_PADDING, false, true>(maps, p, num_sms, stream);
+    case MASK_CAUSAL_KEY_PADDING: return dp::launch<DK, DV, MASK_CAUSAL_KEY_PADDING, false, true>(maps, p, num_sms, stream);
+    case MASK_CAUSAL_CACHE: return dp::launch<DK, DV, MASK_CAUSAL_CACHE, false, true>(maps, p, num_sms, stream);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+cudaError_t launch_fwd_shared(int d_k, int d_v, int mask, const TensorMaps& maps, const FwdParams& p, int num_sms,
+                              cudaStream_t stream)
+{
+    if (d_k == 64 && d_v == 64) return launch_mask<64, 64>(mask, maps, p, num_sms, stream);
+    if (d_k == 128 && d_v == 128) return launch_mask<128, 128>(mask, maps, p, num_sms, stream);
+    if (d_k == 64 && d_v == 128) return launch_mask<64, 128>(mask, maps, p, num_sms, stream);
+    if (d_k == 128 && d_v == 64) return launch_mask<128, 64>(mask, maps, p, num_sms, stream);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace attn

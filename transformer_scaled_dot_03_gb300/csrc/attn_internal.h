@@ -36,32 +36,11 @@ enum : uint32_t {
 
 enum : uint32_t { DEBUG_FORCE_TIMEOUT = 1u };
 
-// Division of x < 2^31 by a fixed d >= 1 as a product: q = x m >> (31 + s), 2^s >= d,
-// m = floor(2^(31 + s) / d) + 1 < 2^32 (Granlund and Montgomery, "Division by invariant
-// integers using multiplication").
-struct Divider {
-    uint32_t m, s;
-
-    explicit Divider(uint32_t d = 1) : m(0), s(0)
-    {
-        while ((1ull << s) < d) ++s;
-        m = static_cast<uint32_t>((1ull << (31 + s)) / d + 1);
-    }
-#ifdef __CUDACC__
-    __device__ __forceinline__ uint32_t divide(uint32_t x) const
-    {
-        return static_cast<uint32_t>(static_cast<uint64_t>(x) * m >> (31 + s));
-    }
-#endif
-};
-
 struct FwdParams {
     int B, H, n, m;
     int causal_off;               // m - n: query row i sees keys j <= i + causal_off (causal masks)
     int num_qblocks;              // ceil(n / rows per work unit)
-    int num_units;                // work units (query tiles, or pairs of them)
-    int paired;                   // a unit pairs query tiles k and num_qblocks - 1 - k (causal masks, enough units)
-    Divider kv_group;             // by the query heads that share a head of K and V
+    int num_units;                // work units (query tiles, paired under the causal masks)
     void* O;                      // bf16 [B,H,n,d_v] (persistent kernel stores rows directly)
     const int32_t* key_lengths;   // device int32 [B] (key-padding masks only)
     float scale_log2;             // scale * log2(e)
@@ -70,6 +49,7 @@ struct FwdParams {
     uint32_t* status;             // device status word
     uint64_t watchdog_ns;         // wall-clock limit of one bounded wait
     uint32_t debug_flags;
+    int kv_group;                 // query heads that share a head of K and V (launch_fwd_shared only)
 };
 
 struct TensorMaps {
@@ -159,6 +139,25 @@ struct DecodeParams {
 // rows: the kernel variant handles n <= rows (1, 2, 4 or 8).
 cudaError_t launch_decode(int d_k, int d_v, int rows, const CUtensorMap& tmK, const CUtensorMap& tmV,
                           const DecodeParams& p, cudaStream_t stream);
+
+// Division of x < 2^31 by a fixed d >= 1 as a product: q = x m >> (31 + s), 2^s >= d,
+// m = floor(2^(31 + s) / d) + 1 < 2^32 (Granlund and Montgomery, "Division by invariant
+// integers using multiplication").
+struct Divider {
+    uint32_t m, s;
+
+    explicit Divider(uint32_t d = 1) : m(0), s(0)
+    {
+        while ((1ull << s) < d) ++s;
+        m = static_cast<uint32_t>((1ull << (31 + s)) / d + 1);
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ uint32_t divide(uint32_t x) const
+    {
+        return static_cast<uint32_t>(static_cast<uint64_t>(x) * m >> (31 + s));
+    }
+#endif
+};
 
 // A key/value cache held in 4 bits (format: attn_cache_q4.cuh).
 struct CacheQ4WriteParams {
@@ -257,6 +256,13 @@ cudaError_t launch_fwd_d128(int mask, const TensorMaps& maps, const FwdParams& p
 // d_k != d_v (64 and 128 either way round).
 cudaError_t launch_fwd_dmix(int d_k, int d_v, int mask, const TensorMaps& maps, const FwdParams& p,
                             int num_sms, cudaStream_t stream);
+// Forward over K and V with fewer heads (p.kv_group), with the distance bias where p.slopes is
+// given; its units are single query tiles.
+cudaError_t launch_fwd_shared(int d_k, int d_v, int mask, const TensorMaps& maps, const FwdParams& p, int num_sms,
+                              cudaStream_t stream);
+// The same with the distance bias (its own translation unit).
+cudaError_t launch_fwd_shared_alibi(int d_k, int d_v, int mask, const TensorMaps& maps, const FwdParams& p, int num_sms,
+                                    cudaStream_t stream);
 // Forward with the linear distance bias (p.slopes), d_k, d_v in {64, 128}.
 cudaError_t launch_fwd_alibi(int d_k, int d_v, int mask, const TensorMaps& maps, const FwdParams& p, int num_sms,
                              cudaStream_t stream);

@@ -125,30 +125,34 @@ struct Unit {
 // K/V in L2. Without a causal mask a unit is one 128-row query tile. With it,
 // a unit pairs query tile k with tile nqb-1-k of the same head (the longest with
 // the shortest), so that every unit visits the same number of key tiles and a
-// plain round-robin over units balances the CTAs; where the pairs are fewer than the
-// CTAs, the tiles go out one by one (4 x 16 heads, 256 rows at the end of up to 4096
-// slots: 59 us in pairs, 64 CTAs).
-__host__ __device__ inline int units_per_head(int num_qblocks, bool paired)
+// plain round-robin over units balances the CTAs.
+//
+// SHARED is the instantiation for K and V whose heads groups of query heads share
+// (p.kv_group; the 4-bit cache read back): its callers have few query tiles against many
+// keys, so its units are single tiles under every mask (4 x 16 heads, 256 rows at the end of up
+// to 4096 slots: 29 us, 59 in pairs, which occupy 64 CTAs). Told apart by a template, since
+// a choice at run time cost the plain causal kernels 0.7 to 4%.
+__host__ __device__ inline int units_per_head(int num_qblocks, int mask)
 {
-    return paired ? (num_qblocks + 1) / 2 : num_qblocks;
+    return mask_is_causal(mask) ? (num_qblocks + 1) / 2 : num_qblocks;
 }
 
-template <int MASK>
+template <int MASK, bool SHARED>
 __device__ __forceinline__ int tiles_of_unit(int u, const FwdParams& p)
 {
-    if (!mask_is_causal(MASK) || !p.paired) return 1;
-    const int k = u % units_per_head(p.num_qblocks, true);
+    if (SHARED || !mask_is_causal(MASK)) return 1;
+    const int k = u % units_per_head(p.num_qblocks, MASK);
     return (k == p.num_qblocks - 1 - k) ? 1 : 2;
 }
 
-template <int MASK>
+template <int MASK, bool SHARED>
 __device__ __forceinline__ Unit tile_of(int u, int i, const FwdParams& p)
 {
     Unit w;
-    const int uph = units_per_head(p.num_qblocks, mask_is_causal(MASK) && p.paired);
+    const int uph = SHARED ? p.num_qblocks : units_per_head(p.num_qblocks, MASK);
     w.bh = u / uph;
     const int k = u % uph;
-    const int qb = mask_is_causal(MASK) ? (i == 0 ? p.num_qblocks - 1 - k : k) : k;
+    const int qb = !SHARED && mask_is_causal(MASK) ? (i == 0 ? p.num_qblocks - 1 - k : k) : k;
     w.q0 = qb * BM;
     w.kv_len = p.m;
     if (mask_has_lengths(MASK)) {
@@ -170,16 +174,16 @@ struct TilePos {
     int u, ti;
 };
 
-template <int MASK>
+template <int MASK, bool SHARED>
 __device__ __forceinline__ void advance(TilePos& t, int u_step, const FwdParams& p)
 {
-    if (++t.ti >= tiles_of_unit<MASK>(t.u, p)) {
+    if (++t.ti >= tiles_of_unit<MASK, SHARED>(t.u, p)) {
         t.ti = 0;
         t.u += u_step;
     }
 }
 
-template <int DK, int DV, int MASK, bool BIAS>
+template <int DK, int DV, int MASK, bool BIAS, bool SHARED>
 __global__ void __launch_bounds__(Layout<DK, DV>::NUM_THREADS, Layout<DK, DV>::CTAS_PER_SM)
 attn_fwd_dp_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
@@ -281,8 +285,8 @@ attn_fwd_dp_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 ++vc;
                 return true;
             };
-            for (TilePos t = first_tile; ok && t.u < p.num_units; advance<MASK>(t, u_step, p)) {
-                const Unit w = tile_of<MASK>(t.u, t.ti, p);
+            for (TilePos t = first_tile; ok && t.u < p.num_units; advance<MASK, SHARED>(t, u_step, p)) {
+                const Unit w = tile_of<MASK, SHARED>(t.u, t.ti, p);
                 if (w.nkv == 0) continue;
                 // the previous tile's Q must have left the buffer
                 if (qc > 0 && !mbar_wait_suspend(bar(L::B_QFREE), static_cast<uint32_t>(qc - 1) & 1u, abort_word,
@@ -295,7 +299,7 @@ attn_fwd_dp_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                     tma_load_3d(sQ + c * CHUNK_BYTES, &tmQ, bar(L::B_QFULL), c * 64, w.q0, w.bh);
                 ++qc;
                 // K(j+1) is issued before V(j): S(j+1) needs it while P(j) is computed
-                const int kv = static_cast<int>(p.kv_group.divide(static_cast<uint32_t>(w.bh)));
+                const int kv = SHARED ? w.bh / p.kv_group : w.bh;
                 ok = load_K(kv, 0);
                 for (int j = 0; ok && j < w.nkv; ++j) {
                     if (j + 1 < w.nkv) ok = load_K(kv, j + 1);
@@ -358,8 +362,8 @@ attn_fwd_dp_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 ++g;
                 return true;
             };
-            for (TilePos t = first_tile; ok && t.u < p.num_units; advance<MASK>(t, u_step, p)) {
-                const Unit w = tile_of<MASK>(t.u, t.ti, p);
+            for (TilePos t = first_tile; ok && t.u < p.num_units; advance<MASK, SHARED>(t, u_step, p)) {
+                const Unit w = tile_of<MASK, SHARED>(t.u, t.ti, p);
                 if (w.nkv == 0) continue;
                 ok = wait(L::Q_IN_TMEM ? L::B_QREADY : L::B_QFULL, static_cast<uint32_t>(qc) & 1u);
                 ++qc;
@@ -435,8 +439,8 @@ attn_fwd_dp_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             return true;
         };
 
-        for (TilePos t = first_tile; ok && t.u < p.num_units; advance<MASK>(t, u_step, p)) {
-            const Unit w = tile_of<MASK>(t.u, t.ti, p);
+        for (TilePos t = first_tile; ok && t.u < p.num_units; advance<MASK, SHARED>(t, u_step, p)) {
+            const Unit w = tile_of<MASK, SHARED>(t.u, t.ti, p);
             const int qrow = w.q0 + r;
             const int qlim = qrow + w.off;   // the row's key position: last key it sees under the causal mask
             // distance-bias slope of the head, log2 domain
@@ -512,8 +516,8 @@ attn_fwd_dp_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 // so that its first S overlaps this epilogue (every MMA of this and the
                 // previous tile is complete, so the Q buffer being overwritten is free)
                 TilePos nt = t;
-                advance<MASK>(nt, u_step, p);
-                while (nt.u < p.num_units && tile_of<MASK>(nt.u, nt.ti, p).nkv == 0) advance<MASK>(nt, u_step, p);
+                advance<MASK, SHARED>(nt, u_step, p);
+                while (nt.u < p.num_units && tile_of<MASK, SHARED>(nt.u, nt.ti, p).nkv == 0) advance<MASK, SHARED>(nt, u_step, p);
                 // (a tile without keys between two with keys finds its successor's Q
                 // already copied by the tile before it)
                 if (nt.u < p.num_units && !(q_done.u == nt.u && q_done.ti == nt.ti)) {
@@ -578,11 +582,11 @@ attn_fwd_dp_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     }
 }
 
-template <int DK, int DV, int MASK, bool BIAS = false>
+template <int DK, int DV, int MASK, bool BIAS = false, bool SHARED = false>
 cudaError_t launch(const TensorMaps& maps, const FwdParams& p, int num_sms, cudaStream_t stream)
 {
     using L = Layout<DK, DV>;
-    auto kern = attn_fwd_dp_kernel<DK, DV, MASK, BIAS>;
+    auto kern = attn_fwd_dp_kernel<DK, DV, MASK, BIAS, SHARED>;
     static bool configured[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
