@@ -137,6 +137,56 @@ def test_read_beyond_the_lengths_ignores_what_lies_there():
     assert torch.isfinite(rk).all()
 
 
+@pytest.mark.parametrize("dk,dv", DIMS)
+def test_write_many_rows_of_a_padded_batch(dk, dv):
+    """Enough rows for the kernel that takes 64 at a time: ragged counts, starts on and off
+    a block's border, before the cache and past its end."""
+    B, H, n, m = 8, 17, 150, 400
+    starts = [0, 64, 37, -70, 399, 251, 2 ** 31 - 100, -200]
+    counts = [150, 150, 100, 150, 150, 149, 150, 150]
+    check_write(garbage(80, B, H, m, dk, dv), rows(81, (B, H, n, dk)), rows(82, (B, H, n, dv)), starts, counts, m)
+
+
+def test_write_many_rows_without_positions():
+    check_write(garbage(83, 2, 40, 300, 64, 128), rows(84, (2, 40, 257, 64)), rows(85, (2, 40, 257, 128)), None, None, 300)
+
+
+@pytest.mark.parametrize("dk,dv", DIMS)
+@pytest.mark.parametrize("group,first,n", [(1, 0, 300), (1, 37, 263), (1, 70, 170), (3, 1, 299)])
+def test_read_many_rows(dk, dv, group, first, n):
+    """Enough rows for the kernels that take 64 at a time; ranges that begin inside a block."""
+    B, H, m = 5, 30, 300
+    x = rows(86, (1, H, m, max(dk, dv)))
+    one = cache_q4.write(garbage(87, 1, H, m, dk, dv).numpy(), x[..., :dk].contiguous(), x[..., :dv].contiguous(), m=m)
+    cache = np.repeat(one, B, 0)
+    lens = [300, 0, 64, 129, 299]
+    wk, wv = cache_q4.read(cache, dk, m, lens)
+    rk, rv = attn.cache_q4_read(torch.from_numpy(cache).cuda(), dk, m, i32(lens), H=H * group, first=first, n=n)
+    torch.cuda.synchronize()
+    for got, want in ((rk, wk), (rv, wv)):
+        assert np.array_equal(got.float().cpu().numpy(), np.repeat(want[:, :, first:first + n], group, 1).astype(np.float32))
+
+
+@pytest.mark.parametrize("B,n", [(2, 3), (64, 200)])
+def test_rows_that_are_only_16_byte_aligned(B, n):
+    """K and V of the writer and the reader 16 bytes off a 32-byte border."""
+    H, m = 3, 200
+    x = rows(88, (B, H, n, 64))
+    off = lambda t: torch.cat([torch.zeros(8, dtype=t.dtype), t.flatten()]).cuda()[8:].view(t.shape)
+    K = off(x)
+    assert K.data_ptr() % 32 == 16
+    cache = garbage(89, B, H, m, 64, 64)
+    want = cache_q4.write(cache[:2].numpy(), x[:2], x[:2], None, None, m)
+    got = cache.cuda()
+    attn.cache_q4_write(got, K, K, m=m)
+    assert np.array_equal(got[:2].cpu().numpy(), want)
+    out = [off(torch.zeros(B, H, n, 64, dtype=torch.bfloat16)) for _ in range(2)]
+    attn.cache_q4_read(got, 64, m, n=n, K=out[0], V=out[1])
+    torch.cuda.synchronize()
+    held = cache_q4.held(x)
+    assert all(np.array_equal(o.double().cpu().numpy(), held) for o in out)
+
+
 def test_offsets_beyond_32_bits():
     """A cache of 4.9 GB: the last block of the last head lies past 2^32 bytes."""
     B, H, m = 1, 40, 64 * 14000

@@ -302,6 +302,60 @@ def test_agrees_with_the_forward_on_the_cache_read_back():
     assert off <= lse_tol + lse_tol_f
 
 
+def test_two_calls_at_once():
+    """Two streams, each with its own workspace, many times over: the bits of a lone call."""
+    cases = [Case(3, 4, 2, 3, 5000, 128, 128, "causal_cache", [5000, 1, 3333], seed=30),
+             Case(4, 2, 4, 1, 7000, 128, 128, "key_padding", [7000, 0, 128, 6001], seed=31)]
+    want = [c.run() for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    Q = [c.Q.cuda() for c in cases]
+    lens = [i32(c.lens) for c in cases]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(20):
+        for k, c in enumerate(cases):
+            outs[k].append(attn.decode_q4(Q[k], c.cache, c.mask, lens[k], m=c.m, stream=streams[k]))
+    torch.cuda.synchronize()
+    for k in range(2):
+        for O, L in outs[k]:
+            assert np.array_equal(O.double().cpu().numpy(), want[k][0]) and np.array_equal(L.double().cpu().numpy(), want[k][1])
+
+
+def test_a_workspace_serves_calls_of_other_sizes_in_turn():
+    """Stale parts and spans of an earlier, larger call are never taken for a later one's."""
+    big = Case(2, 8, 1, 4, 9000, 128, 128, "none", seed=32)
+    small = [Case(1, 1, 1, 1, m, 128, 128, "key_padding", [ln], seed=m) for m, ln in ((9000, 8999), (9000, 65), (200, 130))]
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    for c in small:
+        attn.decode_q4(big.Q.cuda(), big.cache, "none", m=big.m, workspace=ws)
+        O, L = attn.decode_q4(c.Q.cuda(), c.cache, c.mask, i32(c.lens), m=c.m, workspace=ws)
+        torch.cuda.synchronize()
+        Or, Lr, tol, lse_tol = c.reference()
+        off = float((np.abs(O.double().cpu().numpy() - Or) - tol).max())
+        assert off <= 0
+        off = float(np.abs(L.double().cpu().numpy() - Lr).max())
+        assert off <= lse_tol
+
+
+@pytest.mark.parametrize("dk,dv", DIMS)
+@pytest.mark.parametrize("group,n,mask", [(1, 1, "key_padding"), (2, 2, "causal_cache"), (4, 3, "causal_key_padding"),
+                                          (2, 40, "causal_cache")])
+def test_masked_slots_may_hold_anything(dk, dv, group, n, mask):
+    """The same lengths over caches whose other slots hold zeros, random bytes or NaN steps."""
+    m, lens = 700, [700, 129, 64, 1, 0]
+    c = Case(5, 2, group, n, m, dk, dv, mask, lens, seed=33)
+    rand = torch.randint(0, 256, c.cache.shape, generator=torch.Generator().manual_seed(34), dtype=torch.uint8).cuda()
+    K, V = attn.cache_q4_read(c.cache, dk, m, i32(lens))
+    for fill in (torch.zeros_like(rand), rand):
+        c.cache.copy_(fill)
+        attn.cache_q4_write(c.cache, K, V, None, i32(lens), m=m)
+        O, L = c.run()
+        c.cache.fill_(0xFF)
+        attn.cache_q4_write(c.cache, K, V, None, i32(lens), m=m)
+        O2, L2 = c.run()
+        assert np.array_equal(O, O2) and np.array_equal(L, L2) and np.isfinite(O).all()
+
+
 def test_no_slots_and_no_rows():
     cache = attn.cache_q4_empty(2, 2, 0, 64, 64)
     Q = torch.randn(2, 4, 3, 64, device="cuda").to(torch.bfloat16)
