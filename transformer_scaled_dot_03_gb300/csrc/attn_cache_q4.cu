@@ -150,18 +150,49 @@ __device__ __forceinline__ uint2 quantise(const uint32_t (&w)[8], uint32_t* word
     return codes;
 }
 
-// Codes and word of one lane's quarter of group q of the slot k, into the K or V part of its block.
+// Where a lane's quarter group t of group q of slot k lies in the K or V part of a block.
+// Slots 32 apart have the same offsets in rows 32 apart (the format's exchanges look at
+// bits 0 to 2 of the slot), so a lane whose slots step by 32 works them out once.
 template <int D, bool IS_V>
-__device__ __forceinline__ void put(uint8_t* part, int k, int q, int t, uint2 codes, uint32_t word)
-{
-    if (IS_V) {
-        *reinterpret_cast<uint32_t*>(part + q4::v_code_off(k, q, 2 * t, D)) = codes.x;
-        *reinterpret_cast<uint32_t*>(part + q4::v_code_off(k, q, 2 * t + 1, D)) = codes.y;
-    } else {
-        *reinterpret_cast<uint2*>(part + q4::k_code_off(k, q, 2 * t, D)) = codes;
+struct Place {
+    static constexpr int NG = D / q4::GROUP;
+    static constexpr int HALF_CODES = 32 * (D / 2), HALF_WORDS = 32 * 2 * NG;
+    int codes, more, word;                               // V: its two units; K: one of eight bytes
+
+    __device__ __forceinline__ Place(int k, int q, int t)
+    {
+        k &= 31;
+        codes = IS_V ? q4::v_code_off(k, q, 2 * t, D) : q4::k_code_off(k, q, 2 * t, D);
+        more = IS_V ? q4::v_code_off(k, q, 2 * t + 1, D) : codes + 4;
+        word = 32 * D + 2 * (k * NG + q);
     }
-    if (t == 0) *reinterpret_cast<uint16_t*>(part + 32 * D + 2 * (k * (D / q4::GROUP) + q)) = static_cast<uint16_t>(word);
-}
+    // The part's address moved to the half that slot k lies in, for codes and for words.
+    static __device__ __forceinline__ int half_codes(int k) { return k & 32 ? HALF_CODES : 0; }
+    static __device__ __forceinline__ int half_words(int k) { return k & 32 ? HALF_WORDS : 0; }
+
+    __device__ __forceinline__ void store(uint8_t* part, int k, int t, uint2 c, uint32_t w) const
+    {
+        uint8_t* at = part + half_codes(k);
+        if (IS_V) {
+            *reinterpret_cast<uint32_t*>(at + codes) = c.x;
+            *reinterpret_cast<uint32_t*>(at + more) = c.y;
+        } else {
+            *reinterpret_cast<uint2*>(at + codes) = c;
+        }
+        if (t == 0) *reinterpret_cast<uint16_t*>(part + half_words(k) + word) = static_cast<uint16_t>(w);
+    }
+    __device__ __forceinline__ void load(const uint8_t* part, int k, uint2* c, uint32_t* w) const
+    {
+        const uint8_t* at = part + half_codes(k);
+        if (IS_V) {
+            c->x = __ldg(reinterpret_cast<const uint32_t*>(at + codes));
+            c->y = __ldg(reinterpret_cast<const uint32_t*>(at + more));
+        } else {
+            *c = __ldg(reinterpret_cast<const uint2*>(at + codes));
+        }
+        *w = __ldg(reinterpret_cast<const uint16_t*>(part + half_words(k) + word));
+    }
+};
 
 // f(integral constant D, integral constant IS_V) for a side's head dim.
 template <bool IS_V, typename F>
@@ -208,8 +239,10 @@ __global__ void __launch_bounds__(256) cache_q4_write_kernel(const CacheQ4WriteP
     if (slot < 0 || slot >= p.m) return;
     uint8_t* blk = block_of(p, bh, slot);
     const int k = static_cast<int>(slot) % q4::BLOCK;
-    if (is_v) with_dim<true>(d, [&](auto D, auto S) { put<D(), S()>(blk + q4::v_off(p.d_k), k, q, t, codes, word); });
-    else with_dim<false>(d, [&](auto D, auto S) { put<D(), S()>(blk, k, q, t, codes, word); });
+    if (is_v) blk += q4::v_off(p.d_k);
+    auto put = [&](auto D, auto S) { Place<D(), S()>(k, q, t).store(blk, k, t, codes, word); };
+    if (is_v) with_dim<true>(d, put);
+    else with_dim<false>(d, put);
 }
 
 constexpr int TILE = 64;                                 // rows of a CTA
@@ -248,22 +281,24 @@ __global__ void __launch_bounds__(256) cache_q4_write_tile_kernel(const CacheQ4W
     const int64_t slot0 = start + i0 + lo;
     uint8_t* blk0 = block_of(p, bh, slot0);
     const int k0 = static_cast<int>(slot0 % q4::BLOCK);  // the rows' slots lie in this block and the next
+    const int next = q4::block_bytes(p.d_k, p.d_v);
     auto side = [&](auto D, auto S) {
         constexpr int d = D(), ng = d / q4::GROUP;
         const uint8_t* src0 = smem + (S() ? v_at : 0);
         uint8_t* part0 = blk0 + (S() ? q4::v_off(p.d_k) : 0);
-        for (int g0 = 0; g0 < rows * ng; g0 += 64) {     // (whole warps: the quantiser's lanes exchange maxima)
-            const int gi = g0 + static_cast<int>(threadIdx.x / 4u);
-            const bool live = gi < rows * ng;
-            const int r = live ? gi / ng : 0, q = gi % ng;
-            const uint4* src = reinterpret_cast<const uint4*>(src0 + (r * d + q * q4::GROUP + 16 * t) * 2);
+        const int r0 = static_cast<int>(threadIdx.x / 4u) / ng, q = static_cast<int>(threadIdx.x / 4u) % ng;
+        const Place<d, S()> place(k0 + r0, q, t);
+        const uint4* src = reinterpret_cast<const uint4*>(src0 + (r0 * d + q * q4::GROUP + 16 * t) * 2);
+        // 64 groups a round: rows step by 32 or 64. A round runs for the whole CTA, as the quantiser's
+        // lanes exchange maxima; the rows behind the last one lie in shared memory too, and go nowhere.
+        for (int base = 0; base < rows; base += 64 / ng) {
             const uint4 a = src[0], c = src[1];
+            src += 64 / ng * d * 2 / 16;
             const uint32_t w[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
             uint32_t word;
             const uint2 codes = quantise(w, &word);
-            const int k = k0 + r;
-            if (live)
-                put<d, S()>(part0 + (k >= q4::BLOCK ? q4::block_bytes(p.d_k, p.d_v) : 0), k % q4::BLOCK, q, t, codes, word);
+            const int r = base + r0, k = k0 + r;
+            if (r < rows) place.store(part0 + (k >= q4::BLOCK ? next : 0), k, t, codes, word);
         }
     };
     with_dim<false>(p.d_k, side);
@@ -362,33 +397,28 @@ __global__ void __launch_bounds__(256) cache_q4_read_tile_kernel(const CacheQ4Re
     if (p.to_tiles && j0 >= (static_cast<int64_t>(len) + 127) / 128 * 128) return;
     const int rows = min(TILE, p.n - j0);
     const int v_at = TILE * p.d_k * 2;
+    const int live = min(len, p.first + j0 + rows);      // the slots that are read end here
     const uint8_t* base = p.cache + static_cast<int64_t>(bh) * p.blocks * q4::block_bytes(p.d_k, p.d_v);
     auto side = [&](auto D, auto S) {
         constexpr int d = D();
-        const int pieces = rows * (d / 16);
-#pragma unroll 2
-        for (int e = threadIdx.x; e < pieces; e += 256) {
-            const int r = e / (d / 16), piece = e % (d / 16), q = piece >> 2, t = piece & 3;
-            const int slot = p.first + j0 + r;
-            uint2 codes = make_uint2(0u, 0u);
-            uint32_t word = 0u;
-            if (slot < len) {
-                const int k = slot % q4::BLOCK;
-                const uint8_t* part = base + static_cast<int64_t>(slot / q4::BLOCK) * q4::block_bytes(p.d_k, p.d_v) +
-                                      (S() ? q4::v_off(p.d_k) : 0);
-                if (S()) {
-                    codes.x = __ldg(reinterpret_cast<const uint32_t*>(part + q4::v_code_off(k, q, 2 * t, d)));
-                    codes.y = __ldg(reinterpret_cast<const uint32_t*>(part + q4::v_code_off(k, q, 2 * t + 1, d)));
-                } else {
-                    codes = __ldg(reinterpret_cast<const uint2*>(part + q4::k_code_off(k, q, 2 * t, d)));
-                }
-                word = __ldg(reinterpret_cast<const uint16_t*>(part + 32 * d) + k * (d / q4::GROUP) + q);
+        constexpr int step = 256 / (d / 16);             // rows a round: 32 or 64
+        const int r0 = static_cast<int>(threadIdx.x) / (d / 16), piece = static_cast<int>(threadIdx.x) % (d / 16);
+        const Place<d, S()> place((p.first + j0 + r0) % q4::BLOCK, piece >> 2, piece & 3);
+        uint4* dst = reinterpret_cast<uint4*>(smem + (S() ? v_at : 0) + 32 * threadIdx.x);
+        const uint8_t* base0 = base + (S() ? q4::v_off(p.d_k) : 0);
+#pragma unroll
+        for (int u = 0; u < TILE / step; ++u) {          // (rows behind the last one: shared memory that is not stored)
+            const int slot = p.first + j0 + r0 + u * step;
+            uint32_t out[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+            if (slot < live) {
+                uint2 codes;
+                uint32_t word;
+                place.load(base0 + static_cast<int64_t>(slot / q4::BLOCK) * q4::block_bytes(p.d_k, p.d_v), slot, &codes, &word);
+                values(codes, word, out);
             }
-            uint32_t out[8];
-            values(codes, word, out);
-            uint4* dst = reinterpret_cast<uint4*>(smem + (S() ? v_at : 0) + 32 * e);
             dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
             dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+            dst += 256 * 2;
         }
     };
     with_dim<false>(p.d_k, side);
