@@ -197,6 +197,16 @@ def test_a_row_that_sees_only_small_values_next_to_large_ones():
     c.check("small next to large")
 
 
+@pytest.mark.parametrize("dk,dv", DIMS)
+@pytest.mark.parametrize("B,H_kv,group,n,m", [
+    (4, 2, 1, 1, 128), (38, 8, 1, 1, 130), (61, 5, 1, 1, 130), (2, 3, 5, 2, 705), (2, 3, 5, 2, 769), (3, 1, 12, 4, 768)])
+def test_short_caches(dk, dv, B, H_kv, group, n, m):
+    """2 to 13 blocks per pair, 6 to 305 pairs: the pairs that get a CTA each and the next ones that
+    do not; lengths that leave some of a CTA's warps, or all of them, without a block."""
+    lens = [(m - b * 67) % (m + 1) if b % 4 != 3 else b % 3 * 64 for b in range(B)]
+    Case(B, H_kv, group, n, m, dk, dv, "causal_cache", lens, seed=B + m).check(f"B={B} m={m}")
+
+
 @pytest.mark.parametrize("q_scale", [1e-30, 1e-4, 40.0])
 def test_query_magnitudes(q_scale):
     """The fp16 operand of the query rows is scaled by a power of two of their own."""
@@ -212,6 +222,19 @@ def test_rows_with_a_zero_query_take_the_mean():
 
 def test_scale():
     Case(2, 2, 1, 2, 900, 128, 64, "none", seed=10).check("scale", scale=0.31)
+
+
+def test_a_slot_that_cannot_be_held_reaches_every_row_that_sees_it():
+    """Early, in a cut pair's first part, in a CTA's second warp: NaN survives each kind of merge."""
+    for m, at in ((60, 3), (700, 300), (9000, 5), (9000, 8999)):
+        V = rows(12, (1, 2, m, 128))
+        K = rows(11, (1, 2, m, 64))
+        V[0, 0, at, 77] = float("nan")
+        K[0, 1, at, 7] = float("-inf")
+        O, L = Case(1, 2, 2, 1, m, 64, 128, "none", seed=13, K=K, V=V).run()
+        bad = np.isnan(O)
+        assert bad[0, :2, 0, 64:].all() and not bad[0, :2, 0, :64].any() and bad[0, 2:].all(), (m, at)
+        assert np.isfinite(L[0, :2]).all() and np.isnan(L[0, 2:]).all(), (m, at)
 
 
 def test_a_slot_that_cannot_be_held_reaches_only_the_rows_that_see_it():
@@ -369,15 +392,16 @@ def test_no_slots_and_no_rows():
 def test_forced_timeout_reports_and_recovers():
     """The bounded wait of the kernel's warps gives up, the status reports it, and a
     normal call afterwards is right."""
-    c = Case(2, 2, 1, 1, 4096, 128, 128, "none", seed=20)
-    attn.set_watchdog(0, 1)
-    try:
-        attn.decode_q4(c.Q.cuda(), c.cache, "none", m=4096)
-        rc, detail = attn.device_status()
-    finally:
-        attn.set_watchdog(0, 0)
-    assert rc == attn.ATTN_ERR_TIMEOUT and detail & 8
-    c.check("after a timeout")
+    for m in (4096, 700):                                 # shares of all blocks; a CTA per pair
+        c = Case(2, 2, 1, 1, m, 128, 128, "none", seed=20)
+        attn.set_watchdog(0, 1)
+        try:
+            attn.decode_q4(c.Q.cuda(), c.cache, "none", m=m)
+            rc, detail = attn.device_status()
+        finally:
+            attn.set_watchdog(0, 0)
+        assert rc == attn.ATTN_ERR_TIMEOUT and detail & 8
+        c.check("after a timeout")
 
 
 def test_binding_refusals():

@@ -979,6 +979,12 @@ namespace {
 
 constexpr int kQ4MaxRows = 64;            // rows per cache head up to which the few-row kernel runs
 constexpr int kQ4WholeBlocks = 2;         // up to this many blocks per (b, cache head) a warp takes whole pairs
+// Two to kQ4CtaBlocks blocks and at most kQ4CtaPairs pairs (the CTA slots of 152 SMs): a CTA per
+// pair. B x 8 heads, lengths m/2..m, us with a CTA per pair and with shares (one launch more):
+// 64/64, B = 16: m 256 3.6 / 7.4, m 512 4.6 / 7.2; B = 32: m 512 5.4 / 8.5; 128/128, B = 8:
+// m 512 6.2 / 8.1, m 1024 8.9 / 8.5, m 1536 12.2 / 9.7; 512 pairs: m 128 6.7 / 4.8, m 512 10.0 / 10.5.
+constexpr int kQ4CtaBlocks = 12;
+constexpr int64_t kQ4CtaPairs = 304;
 
 // Bound on the kernel's warps, used to size the workspace.
 int64_t q4_max_warps(int tile_rows) { return tile_rows == 8 ? 2048 : 1280; }
@@ -996,11 +1002,12 @@ int q4_blocks(int m) { return static_cast<int>((static_cast<int64_t>(m) + attn::
 
 // Scratch of attn_decode_q4: the parts of split pairs, or for many rows K and V as bf16.
 struct Q4Plan {
-    bool few, split;
+    bool few;
+    int mode;                         // few: attn::Q4_*
     int rows, row_tiles;              // rows per cache head, tiles of them
     int64_t pairs, warps;             // (b, cache head, row tile) triples; most workers
     int part_rows;
-    size_t ml_off, pairs_off;         // split
+    size_t ml_off, pairs_off;         // Q4_SHARES
     size_t v_off;                     // many rows
     size_t total;
 };
@@ -1020,9 +1027,11 @@ Q4Plan q4_plan(int64_t B, int64_t H, int64_t H_kv, int64_t n, int m, int d_k, in
     w.row_tiles = (w.rows + tile - 1) / tile;
     w.pairs = B * H_kv * w.row_tiles;
     const int64_t blocks = q4_blocks(m);
-    w.split = blocks > kQ4WholeBlocks;
-    w.warps = std::min(q4_max_warps(tile), w.split ? w.pairs * blocks : w.pairs);
-    if (!w.split) return w;
+    w.mode = blocks > 1 && blocks <= kQ4CtaBlocks && w.pairs <= kQ4CtaPairs ? attn::Q4_CTA
+             : blocks <= kQ4WholeBlocks                                     ? attn::Q4_WHOLE
+                                                                            : attn::Q4_SHARES;
+    w.warps = std::min(q4_max_warps(tile), w.mode == attn::Q4_SHARES ? w.pairs * blocks : w.pairs);
+    if (w.mode != attn::Q4_SHARES) return w;
     w.part_rows = std::min(w.rows, tile);
     const size_t parts = static_cast<size_t>(2 * w.warps) * w.part_rows;
     w.ml_off = round_up(parts * d_v * 4, kWsAlign);
@@ -1181,7 +1190,7 @@ extern "C" int attn_decode_q4(const void* Q, const void* cache, int B, int H, in
     p.key_lengths = lens;
     p.slopes = slopes;
     p.scale_log2 = static_cast<float>(sc * 1.4426950408889634074);
-    p.split = w.split ? 1 : 0;
+    p.mode = w.mode;
     int num_sms = 0;
     if ((rc = sm_count(&num_sms)) != ATTN_OK) return rc;
     p.warps = static_cast<int>(std::min<int64_t>(

@@ -194,7 +194,11 @@ struct CacheQ4ReadParams {
 cudaError_t launch_cache_q4_write(const CacheQ4WriteParams& p, cudaStream_t stream);
 cudaError_t launch_cache_q4_read(const CacheQ4ReadParams& p, cudaStream_t stream);
 
-// Few-row attention over that cache (attn_kernel_decode_q4.cuh).
+// Few-row attention over that cache (attn_kernel_decode_q4.cuh). How the (entry, cache
+// head, row tile) pairs are divided: equal shares of all blocks per warp, with parts merged by a
+// second kernel; whole pairs per warp; or a CTA per pair.
+enum { Q4_SHARES = 0, Q4_WHOLE = 1, Q4_CTA = 2 };
+
 struct DecodeQ4Params {
     const uint16_t* Q;            // bf16 [B,H_kv,R,d_k]: the R = group * n rows that share a cache head
     const uint8_t* cache;
@@ -206,11 +210,11 @@ struct DecodeQ4Params {
     const int32_t* key_lengths;   // device int32 [B] (key-padding masks only)
     const float* slopes;          // fp32 [H]: distance-bias slope per query head, or null
     float scale_log2;             // scale * log2(e)
-    int split;                    // 1: equal shares of all blocks per warp, parts merged after; 0: whole pairs
-    int warps;                    // workers
+    int mode;                     // Q4_*
+    int warps;                    // workers (Q4_SHARES, Q4_WHOLE)
     uint16_t* O;                  // bf16 [B,H,n,d_v]
     float* LSE;                   // fp32 [B,H,n] or null
-    float* part_o;                // fp32 [2 warps][part_rows][d_v] (split)
+    float* part_o;                // fp32 [2 warps][part_rows][d_v] (Q4_SHARES)
     float* part_ml;               // fp32 [2 warps][part_rows][2]: max (log2 domain), sum
     int2* pair_parts;             // [pairs]: first and last worker of a cut pair, (-1, 0) for a whole one
     int part_rows;

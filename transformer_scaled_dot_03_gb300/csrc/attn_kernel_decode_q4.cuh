@@ -46,9 +46,13 @@
 // with an online softmax of its own. A pair that lies in one warp's range is written there;
 // of one that is cut, each warp writes its part (max, sum, unnormalised O) to its slot 0
 // (the pair began in an earlier warp) or slot 1, and a second kernel merges the parts in
-// order. (A CTA per pair, its warps merging in shared memory, spent 6 us per pair on
-// latencies that nothing covered; chunks that an SM's warps take in turn cost more in
-// pair starts than the better balance gives.)
+// order. (Chunks that an SM's warps take in turn cost more in pair starts than the
+// better balance gives.)
+//
+// Few short pairs (Q4_CTA) take a CTA each, whose warps divide the pair's blocks and merge
+// their parts in shared memory: one launch and no workspace. With more pairs than CTA slots
+// its latencies (6 us per pair) would not be covered, and short pairs then go whole to a
+// warp each (Q4_WHOLE).
 #pragma once
 
 #include <cstdint>
@@ -78,6 +82,7 @@ struct Layout {
     // 2 blocks of 8704 or 6528 bytes, or 3 of 4352, in flight per warp
     static constexpr int STAGES = DK + DV == 128 ? 3 : 2;
     static constexpr int RING = WARPS * STAGES * BYTES_BLOCK;
+    static_assert(ROWS * (DV + 2) * 4 <= STAGES * BYTES_BLOCK, "a warp's part fits its ring");
     static constexpr int ROW_OFF = RING;                  // per warp and row: RowInfo
     static constexpr int BAR_OFF = ROW_OFF + WARPS * ROWS * 16;
     static constexpr int MISC_OFF = BAR_OFF + (WARPS * STAGES + 1) * 8;
@@ -134,8 +139,6 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
 
 // 2^e for e in [-126, 127].
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
-// Exponent of a finite positive x (subnormals: -127).
-__device__ __forceinline__ int exponent(float x) { return static_cast<int>((__float_as_uint(x) >> 23) & 255u) - 127; }
 
 // Step of group q in a slot's words (u0, in the low bits, masked off).
 __device__ __forceinline__ float word_step(uint32_t w, int q) { return __uint_as_float((q ? w : w << 16) & 0xFFF00000u); }
@@ -162,7 +165,7 @@ __device__ __forceinline__ int pair_blocks(const DecodeQ4Params& p, int b)
 }
 
 // A place in the sequence: block blk of nb of pair pr of entry b, whose pairs begin at
-// unit `before`; units left to take (with `split` blocks and pair starts, else pairs).
+// unit `before`; units left to take (blocks and pair starts, or whole pairs in Q4_WHOLE).
 struct Cursor {
     int b, pr, blk, nb, todo;
     uint32_t before;
@@ -170,14 +173,14 @@ struct Cursor {
     // Past `blocks` blocks of the pair.
     __device__ __forceinline__ void next(const DecodeQ4Params& p, int pairs_b, int blocks)
     {
-        if (p.split) todo -= blocks;
+        if (p.mode != Q4_WHOLE) todo -= blocks;
         blk += blocks;
         if (blk < nb) return;
         --todo;                                          // the next pair's start, or the pair itself
         blk = 0;
         if (++pr == pairs_b) {
             pr = 0;
-            before += static_cast<uint32_t>(p.split ? nb + 1 : 1) * pairs_b;
+            before += static_cast<uint32_t>(p.mode != Q4_WHOLE ? nb + 1 : 1) * pairs_b;
             ++b;
             if (todo > 0) nb = pair_blocks(p, b);
         }
@@ -205,7 +208,7 @@ __device__ __forceinline__ Cursor first_block(const DecodeQ4Params& p, int w, in
     c.before = 0;
     constexpr int HELD = 4;                              // entries per lane that are looked at once
     int nb[HELD];
-    const bool ragged = p.split && mask_has_lengths(p.mask);
+    const bool ragged = p.mode == Q4_SHARES && mask_has_lengths(p.mask);
     uint32_t total;
     if (ragged) {
         uint32_t sum = 0;
@@ -218,14 +221,14 @@ __device__ __forceinline__ Cursor first_block(const DecodeQ4Params& p, int w, in
         for (int i = 32 * HELD + lane; i < p.B; i += 32) sum += (pair_blocks(p, i) + 1) * pairs_b;
         total = __reduce_add_sync(0xffffffffu, sum);
     } else {
-        total = static_cast<uint32_t>(p.B) * pairs_b * (p.split ? pair_blocks(p, 0) + 1 : 1);
+        total = static_cast<uint32_t>(p.B) * pairs_b * (p.mode == Q4_SHARES ? pair_blocks(p, 0) + 1 : 1);
     }
     shares->each = total / p.warps;
     shares->more = total - shares->each * p.warps;
     uint32_t u0 = shares->each * w + min(static_cast<uint32_t>(w), shares->more);
     c.todo = static_cast<int>(shares->each + (static_cast<uint32_t>(w) < shares->more ? 1u : 0u));
     if (c.todo == 0) return c;
-    if (!p.split) {
+    if (p.mode == Q4_WHOLE) {
         c.b = static_cast<int>(u0 / pairs_b);
         c.before = static_cast<uint32_t>(c.b) * pairs_b;
         c.pr = static_cast<int>(u0 - c.before);
@@ -274,7 +277,7 @@ __device__ __forceinline__ Cursor first_block(const DecodeQ4Params& p, int w, in
     return c;
 }
 
-template <int DK, int DV, int NT, bool PACK>
+template <int DK, int DV, int NT, bool PACK, bool CTA>
 __global__ void __launch_bounds__(THREADS, decode_q4_ctas_per_sm(DK, DV, 8 * NT))
 attn_decode_q4_kernel(const DecodeQ4Params p)
 {
@@ -302,10 +305,23 @@ attn_decode_q4_kernel(const DecodeQ4Params p)
 
     // consecutive workers sit in different CTAs, so that little work spreads over the SMs
     const int worker = warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
-    if (worker >= p.warps) return;
     const int pairs_b = p.H_kv * p.row_tiles;            // pairs per entry
     Shares shares;
-    Cursor at = first_block(p, worker, lane, pairs_b, &shares);
+    Cursor at;
+    if constexpr (CTA) {                                 // a quarter of the CTA's pair
+        at.b = static_cast<int>(blockIdx.x) / pairs_b;
+        at.pr = static_cast<int>(blockIdx.x) - at.b * pairs_b;
+        at.nb = pair_blocks(p, at.b);
+        at.blk = at.nb * warp / WARPS;
+        at.todo = at.nb * (warp + 1) / WARPS - at.blk;
+        at.before = 0;
+        shares.each = shares.more = 0;
+    } else {
+        if (worker >= p.warps) return;
+        at = first_block(p, worker, lane, pairs_b, &shares);
+    }
+    const Cursor start = at;
+    float* const own = reinterpret_cast<float*>(smem + warp * L::STAGES * L::BYTES_BLOCK);   // Q4_CTA: this warp's part
     Cursor ahead = at;                                   // the next block to copy
     uint32_t landed = 0, issued = 0;                     // blocks consumed, copies issued
     auto issue = [&]() {
@@ -340,7 +356,7 @@ attn_decode_q4_kernel(const DecodeQ4Params p)
         const int64_t pair_bh = static_cast<int64_t>(at.b) * p.H_kv + hk;
         const int64_t pair = pair_bh * p.row_tiles + rt;
         const int nb = at.nb;
-        const int last = p.split ? min(nb, at.blk + at.todo) : nb;   // one past its last block here
+        const int last = CTA || p.mode != Q4_WHOLE ? min(nb, at.blk + at.todo) : nb;   // one past its last block here
         int kv_len;
         const int end = visible_end(p, at.b, &kv_len);   // slots past it are seen by no row
         const int off = causal_offset(p.mask, p.m - p.n, kv_len, p.n);
@@ -718,8 +734,11 @@ attn_decode_q4_kernel(const DecodeQ4Params p)
 
         // -------------------------------------------- write the pair, or this warp's part of it
         const bool ends = last == nb;
-        const bool whole = ends && !mid_pair;
+        const bool whole = ends && !mid_pair && !CTA;
         const int64_t part0 = static_cast<int64_t>(2 * worker + (mid_pair ? 0 : 1)) * p.part_rows;
+        // (the ring is free: Q4_CTA has one pair, and every lane is done with its last block)
+        float* const part_ml = CTA ? own : p.part_ml + 2 * part0;
+        float* const part_o = CTA ? own + 2 * L::ROWS : p.part_o + part0 * DV;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -758,20 +777,20 @@ attn_decode_q4_kernel(const DecodeQ4Params p)
                         w.w = pack_bf16x2(v[6], v[7]);
                         *reinterpret_cast<uint4*>(p.O + orow * DV + 64 * q + 8 * g) = w;
                     } else {
-                        float4* dst = reinterpret_cast<float4*>(p.part_o + (part0 + row) * DV + 64 * q + 8 * g);
+                        float4* dst = reinterpret_cast<float4*>(part_o + row * DV + 64 * q + 8 * g);
                         dst[0] = make_float4(v[0], v[1], v[2], v[3]);
                         dst[1] = make_float4(v[4], v[5], v[6], v[7]);
                     }
                 }
                 if (g == 0 && (!PACK || t < 2)) {
                     if (!whole) {
-                        *reinterpret_cast<float2*>(p.part_ml + 2 * (part0 + row)) = make_float2(m_run[nt][c], l);
+                        *reinterpret_cast<float2*>(part_ml + 2 * row) = make_float2(m_run[nt][c], l);
                     } else if (p.LSE != nullptr) {
                         p.LSE[orow] = l == 0.f ? -INFINITY : (m_use + __log2f(l)) * LN2;
                     }
                 }
             }
-        if (p.split && lane == 0 && !mid_pair) {
+        if (!CTA && p.mode == Q4_SHARES && lane == 0 && !mid_pair) {
             // (the pair's last block is unit nb of it)
             const uint32_t u = at.before + static_cast<uint32_t>(at.pr) * (nb + 1) + nb;
             p.pair_parts[pair] = whole ? make_int2(-1, 0) : make_int2(worker, static_cast<int>(shares.worker_of(u)));
@@ -784,6 +803,38 @@ attn_decode_q4_kernel(const DecodeQ4Params p)
         for (uint32_t i = landed; i < issued; ++i)
             while (!mbar_test(bar0 + 8u * (i % L::STAGES), (i / L::STAGES) & 1u) && globaltimer_ns() - t0 < 100000000ull) {
             }
+    }
+    if (!CTA) return;
+
+    // -------------------------------------------- Q4_CTA: merge the warps' parts
+    if (start.todo == 0 || !ok)                          // no part
+        for (int r = lane; r < L::ROWS; r += 32) *reinterpret_cast<float2*>(own + 2 * r) = make_float2(-INFINITY, 0.f);
+    __syncthreads();
+    const int64_t pair_bh = static_cast<int64_t>(start.b) * p.H_kv + start.pr / p.row_tiles;
+    const int r0 = start.pr % p.row_tiles * L::ROWS, rows = min(L::ROWS, p.R - r0);
+    for (int e = threadIdx.x; e < rows * (DV / 2); e += THREADS) {
+        const int row = e / (DV / 2), c = e % (DV / 2) * 2;
+        float2 ml[WARPS];
+        float M = -INFINITY, Lsum = 0.f, v0 = 0.f, v1 = 0.f;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+            ml[w] = *reinterpret_cast<const float2*>(smem + w * L::STAGES * L::BYTES_BLOCK + 8 * row);
+            M = fmaxf(M, ml[w].x);
+        }
+        const float M_use = M == -INFINITY ? 0.f : M;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+            if (ml[w].x == -INFINITY && ml[w].y == 0.f) continue;              // no part, or no visible slot in it
+            const float f = ex2_approx(ml[w].x - M_use);
+            const float2 x = *reinterpret_cast<const float2*>(smem + w * L::STAGES * L::BYTES_BLOCK + 8 * L::ROWS + 4 * (row * DV + c));
+            Lsum = fmaf(ml[w].y, f, Lsum);
+            v0 = fmaf(x.x, f, v0);
+            v1 = fmaf(x.y, f, v1);
+        }
+        const int64_t orow = pair_bh * p.R + r0 + row;
+        const float inv = Lsum == 0.f ? 0.f : 1.f / Lsum;                      // (a NaN sum is not 0: it reaches the output)
+        *reinterpret_cast<uint32_t*>(p.O + orow * DV + c) = pack_bf16x2(v0 * inv, v1 * inv);
+        if (c == 0 && p.LSE != nullptr) p.LSE[orow] = Lsum == 0.f ? -INFINITY : (M_use + __log2f(Lsum)) * LN2;
     }
 }
 
@@ -900,11 +951,11 @@ attn_decode_q4_merge_kernel(const DecodeQ4Params p, int tile_rows)
     if (lane == 0 && p.LSE != nullptr) p.LSE[orow] = Lsum == 0.f ? -INFINITY : (M_use + __log2f(Lsum)) * LN2;
 }
 
-template <int DK, int DV, int NT, bool PACK>
+template <int DK, int DV, int NT, bool PACK, bool CTA>
 cudaError_t launch(const DecodeQ4Params& p, cudaStream_t stream)
 {
     using L = Layout<DK, DV, NT, PACK>;
-    auto kern = attn_decode_q4_kernel<DK, DV, NT, PACK>;
+    auto kern = attn_decode_q4_kernel<DK, DV, NT, PACK, CTA>;
     static bool configured[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -915,9 +966,10 @@ cudaError_t launch(const DecodeQ4Params& p, cudaStream_t stream)
         if (e != cudaSuccess) return e;
         configured[dev] = true;
     }
-    const unsigned ctas = static_cast<unsigned>((p.warps + WARPS - 1) / WARPS);
+    const unsigned ctas = CTA ? static_cast<unsigned>(p.B) * p.H_kv * p.row_tiles
+                              : static_cast<unsigned>((p.warps + WARPS - 1) / WARPS);
     e = launch_pdl(kern, dim3(ctas), dim3(THREADS), L::BYTES, stream, p);
-    if (e != cudaSuccess || !p.split) return e;
+    if (e != cudaSuccess || CTA || p.mode != Q4_SHARES) return e;
     const int64_t items = static_cast<int64_t>(p.B) * p.H_kv * p.row_tiles * p.part_rows;
     const int per = MERGE_WARPS / p.merge_warps;
     return launch_pdl(attn_decode_q4_merge_kernel<DV>, dim3(static_cast<unsigned>((items + per - 1) / per)),
