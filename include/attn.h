@@ -351,7 +351,9 @@ int attn_merge_proj(const void* O, const void* W_o, const void* bias, int B, int
  *   distance bias of attn_fwd_alibi. Up to 64 rows per cache head (n H / H_kv) take a
  *   kernel that streams the cache once per 16 rows, its blocks dealt out evenly over the SMs as
  *   the lengths on the device have them; more rows read the cache into the workspace
- *   and run the tensor-core forward. The workspace (caller-owned, 256-byte aligned, at
+ *   and run the tensor-core forward, whose key tiles are dealt out in the same way where
+ *   the query tiles alone would not fill the SMs. The first call on a device allocates a status
+ *   word: make one before a stream capture. The workspace (caller-owned, 256-byte aligned, at
  *   least attn_decode_q4_workspace_size(...) bytes, contents on entry do not matter; 0
  *   for short caches) belongs to one call at a time: calls that may overlap need one
  *   each. O and LSE do not depend on the order in which CTAs run.

@@ -165,6 +165,18 @@ def test_many_rows(dk, dv, mask, group, n):
         f"{mask} n={n}", many=True)
 
 
+@pytest.mark.parametrize("dk,dv", DIMS)
+@pytest.mark.parametrize("B,H_kv,group,n,m,mask", [
+    (1, 1, 1, 65, 40000, "none"), (3, 2, 4, 100, 4000, "causal_cache"), (40, 1, 1, 70, 2600, "key_padding"),
+    (2, 1, 2, 300, 4100, "causal"), (6, 1, 8, 130, 3333, "causal_key_padding")])
+def test_many_rows_over_a_long_cache(dk, dv, B, H_kv, group, n, m, mask):
+    """The key tiles cut into shares: units cut several times, whole ones, ones without a key;
+    one part of a unit that a row sees nothing of."""
+    lens = [(m, 0, 2 * m // 3, 1, n - 30, 129)[b % 6] - b // 6 % 2 for b in range(B)] if mask in inputs.LENGTH_MASKS else None
+    lens = lens and [max(x, 0) for x in lens]
+    Case(B, H_kv, group, n, m, dk, dv, mask, lens, seed=m + n, slopes=n == 300).check(f"{mask} n={n} m={m}", many=True)
+
+
 @pytest.mark.parametrize("B,H_kv,group,lens", [
     (1, 1, 1, [40000]), (70, 3, 2, None), (5, 1, 1, [1, 40000, 0, 2, 9000]), (300, 1, 1, None)])
 def test_uneven_shares(B, H_kv, group, lens):
@@ -392,8 +404,9 @@ def test_no_slots_and_no_rows():
 def test_forced_timeout_reports_and_recovers():
     """The bounded wait of the kernel's warps gives up, the status reports it, and a
     normal call afterwards is right."""
-    for m in (4096, 700):                                 # shares of all blocks; a CTA per pair
-        c = Case(2, 2, 1, 1, m, 128, 128, "none", seed=20)
+    # shares of all blocks; a CTA per pair; many rows in shares of the key tiles
+    for m, n in ((4096, 1), (700, 1), (4096, 100)):
+        c = Case(2, 2, 1, n, m, 128, 128, "none", seed=20)
         attn.set_watchdog(0, 1)
         try:
             attn.decode_q4(c.Q.cuda(), c.cache, "none", m=m)
@@ -401,7 +414,7 @@ def test_forced_timeout_reports_and_recovers():
         finally:
             attn.set_watchdog(0, 0)
         assert rc == attn.ATTN_ERR_TIMEOUT and detail & 8
-        c.check("after a timeout")
+        c.check("after a timeout", many=n > 64)
 
 
 def test_binding_refusals():

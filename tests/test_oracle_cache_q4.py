@@ -164,7 +164,7 @@ def test_sizes(lib):
     assert lib.attn_cache_q4_size(64, 16, 8192, 128, 128) * 64 == 64 * 16 * 8192 * 512 * 17
     assert attn.decode_q4_workspace_size(8, 8, 8, 1, 64, 64, 64) == 0
     # many rows: the cache as bf16
-    assert attn.decode_q4_workspace_size(2, 8, 4, 100, 4096, 128, 64) == 2 * 4 * 4096 * 192 * 2
+    assert attn.decode_q4_workspace_size(256, 8, 4, 100, 4096, 128, 64) == 256 * 4 * 4096 * 192 * 2
     # few rows: bounded however large the batch and the cache are
     assert attn.decode_q4_workspace_size(512, 32, 8, 8, 131072, 128, 128) < 64 << 20
 

@@ -205,10 +205,12 @@ int fill_no_keys(int64_t bh, int n, int d_v, void* O, float* LSE, cudaStream_t s
 // Tensor maps, parameters and the launch of the attention kernel (m >= 1),
 // with `status` as the kernel's device status word; `slopes` (device fp32 [H])
 // selects the kernel with the linear distance bias, null the plain one. kv_group > 0: K and V
-// have H / kv_group heads, each shared by kv_group query heads (launch_fwd_shared).
+// have H / kv_group heads, each shared by kv_group query heads (launch_fwd_shared); shares, if
+// given, holds the fields for equal shares of the key tiles.
 int launch_attention(const void* Q, const void* K, const void* V, int B, int H, int n, int m, int d_k,
                      int d_v, int mask_kind, const int32_t* key_lengths, float scale, void* O, float* LSE,
-                     uint32_t* status, cudaStream_t st, const float* slopes = nullptr, int kv_group = 0)
+                     uint32_t* status, cudaStream_t st, const float* slopes = nullptr, int kv_group = 0,
+                     const attn::FwdParams* shares = nullptr)
 {
     const int64_t bh = static_cast<int64_t>(B) * H;
     const int64_t num_qblocks = (static_cast<int64_t>(n) + 127) / 128;
@@ -227,7 +229,8 @@ int launch_attention(const void* Q, const void* K, const void* V, int B, int H, 
                                                              : 1.0 / std::sqrt(static_cast<double>(d_k));
     // causal units pair two query tiles (not in the kernel for shared heads)
     const bool paired = attn::mask_is_causal(mask_kind) && kv_group == 0;
-    attn::FwdParams p;
+    attn::FwdParams p = {};
+    if (shares != nullptr) p = *shares;
     p.B = B;
     p.H = H;
     p.n = n;
@@ -985,6 +988,13 @@ constexpr int kQ4WholeBlocks = 2;         // up to this many blocks per (b, cach
 // m 512 6.2 / 8.1, m 1024 8.9 / 8.5, m 1536 12.2 / 9.7; 512 pairs: m 128 6.7 / 4.8, m 512 10.0 / 10.5.
 constexpr int kQ4CtaBlocks = 12;
 constexpr int64_t kQ4CtaPairs = 304;
+// Many rows: whole query tiles go round the CTAs in ceil(units / CTAs) turns of up to `tiles` key
+// tiles; equal shares take units (tiles + SHARE_START) / CTAs and kQ4ShareCost tiles' time more (the
+// parts' way to memory, the kernel that joins them). 16 heads, lengths m/2..m, 128/128, us in
+// turns and in shares: 1 x 128 rows, m 1024 13.1 / 15.0, m 2048 20.0 / 16.6, m 16384 111 / 30;
+// 1 x 512, m 2048 20.3 / 20.4, m 4096 33.8 / 26.9; 4 x 512, m 4096 57.0 / 56.9, m 16384 201 / 172;
+// 8 x 512, m 16384 (four turns, which even out by themselves) 340 / 358.
+constexpr int kQ4ShareCost = 8;
 
 // Bound on the kernel's warps, used to size the workspace.
 int64_t q4_max_warps(int tile_rows) { return tile_rows == 8 ? 2048 : 1280; }
@@ -1009,6 +1019,8 @@ struct Q4Plan {
     int part_rows;
     size_t ml_off, pairs_off;         // Q4_SHARES
     size_t v_off;                     // many rows
+    int fwd_ctas;                     // > 0: the forward with equal shares of the key tiles
+    size_t fwd_o_off, fwd_ml_off, fwd_units_off;
     size_t total;
 };
 
@@ -1020,6 +1032,15 @@ Q4Plan q4_plan(int64_t B, int64_t H, int64_t H_kv, int64_t n, int m, int d_k, in
     if (!w.few) {
         w.v_off = round_up(static_cast<size_t>(B * H_kv) * m * d_k * 2, kWsAlign);
         w.total = w.v_off + round_up(static_cast<size_t>(B * H_kv) * m * d_v * 2, kWsAlign);
+        const int64_t units = B * H * ((n + 127) / 128), tiles = (static_cast<int64_t>(m) + 127) / 128;
+        const int64_t slots = d_k == 64 && d_v == 64 ? 304 : 152;
+        const int64_t turns = (units + slots - 1) / slots, shared = units * (tiles + attn::SHARE_START);
+        if (turns > 2 || turns * tiles <= shared / slots + kQ4ShareCost || shared > INT32_MAX) return w;
+        w.fwd_ctas = static_cast<int>(slots);
+        w.fwd_o_off = w.total;
+        w.fwd_ml_off = w.fwd_o_off + static_cast<size_t>(2 * w.fwd_ctas) * 128 * d_v * 4;
+        w.fwd_units_off = w.fwd_ml_off + static_cast<size_t>(2 * w.fwd_ctas) * 128 * 8;
+        w.total = w.fwd_units_off + round_up(static_cast<size_t>(units) * 8, kWsAlign);
         return w;
     }
     const int tile = attn::decode_q4_tile_rows(static_cast<int>(R));
@@ -1170,8 +1191,13 @@ extern "C" int attn_decode_q4(const void* Q, const void* cache, int B, int H, in
         // many rows: the cache as bf16 (as far as the forward's 128-key tiles go), then the tensor-core forward
         rc = q4_read(cache, B, H_kv, H_kv, m, 0, m, d_k, d_v, lens, wsb, wsb + w.v_off, st, true);
         if (rc != ATTN_OK) return rc;
+        attn::FwdParams shares = {};
+        shares.ctas = w.fwd_ctas;
+        shares.part_o = reinterpret_cast<float*>(wsb + w.fwd_o_off);
+        shares.part_ml = reinterpret_cast<float2*>(wsb + w.fwd_ml_off);
+        shares.unit_parts = reinterpret_cast<int2*>(wsb + w.fwd_units_off);
         return launch_attention(Q, wsb, wsb + w.v_off, B, H, n, m, d_k, d_v, mask_kind, lens, scale, O, LSE, status, st,
-                                slopes, H / H_kv);
+                                slopes, H / H_kv, &shares);
     }
 
     const double sc = (scale > 0.f && std::isfinite(scale)) ? static_cast<double>(scale)

@@ -49,7 +49,12 @@ struct FwdParams {
     uint32_t* status;             // device status word
     uint64_t watchdog_ns;         // wall-clock limit of one bounded wait
     uint32_t debug_flags;
-    int kv_group;                 // query heads that share a head of K and V (launch_fwd_shared only)
+    // launch_fwd_shared only:
+    int kv_group;                 // query heads that share a head of K and V
+    int ctas;                     // > 0: at most this many CTAs, each with an equal share of the key tiles
+    float* part_o;                // fp32 [2 ctas][4][d_v/4][32][4]
+    float2* part_ml;              // [2 ctas][128] maximum, sum
+    int2* unit_parts;             // [units] first and last CTA
 };
 
 struct TensorMaps {
@@ -260,6 +265,8 @@ cudaError_t launch_fwd_d128(int mask, const TensorMaps& maps, const FwdParams& p
 // d_k != d_v (64 and 128 either way round).
 cudaError_t launch_fwd_dmix(int d_k, int d_v, int mask, const TensorMaps& maps, const FwdParams& p,
                             int num_sms, cudaStream_t stream);
+// Tiles that a unit's start counts as when the key tiles are cut into equal shares (p.ctas).
+constexpr int SHARE_START = 3;
 // Forward over K and V with fewer heads (p.kv_group), with the distance bias where p.slopes is
 // given; its units are single query tiles.
 cudaError_t launch_fwd_shared(int d_k, int d_v, int mask, const TensorMaps& maps, const FwdParams& p, int num_sms,

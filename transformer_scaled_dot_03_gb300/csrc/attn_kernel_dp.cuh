@@ -119,6 +119,8 @@ __device__ __forceinline__ bool drain_wait(uint32_t bar, uint32_t parity, uint64
 struct Unit {
     int bh, q0, kv_len, nkv;
     int off;   // query row i sits at key position i + off (the causal masks' diagonal)
+    int j0;    // first key tile, and whether these are all of them (SHARED; else 0, true)
+    bool whole;
 };
 
 // Work units are numbered head-major so that concurrently running units share
@@ -130,8 +132,16 @@ struct Unit {
 // SHARED is the instantiation for K and V whose heads groups of query heads share
 // (p.kv_group; the 4-bit cache read back): its callers have few query tiles against many
 // keys, so its units are single tiles under every mask (4 x 16 heads, 256 rows at the end of up
-// to 4096 slots: 29 us, 59 in pairs, which occupy 64 CTAs). Told apart by a template, since
+// up to 4096 slots: 29 us, 59 in pairs, which occupy 64 CTAs). Told apart by a template, since
 // a choice at run time cost the plain causal kernels 0.7 to 4%.
+//
+// With p.ctas > 0 (SHARED) the key tiles of all units, in order, are cut into equal shares, one per
+// CTA, as the lengths on the device have them; a unit's start (writing out the one before, 3 us) counts
+// as START tiles. A CTA then has at most two parts of cut units
+// (the one it begins in the middle of: slot 2c, the one it leaves unfinished: 2c + 1): their O,
+// maximum and sum stay in fp32 in the workspace, the CTA with a unit's first tile notes
+// which CTAs have parts of it, and attn_fwd_merge_kernel joins them. A unit without
+// a visible key counts as one tile.
 __host__ __device__ inline int units_per_head(int num_qblocks, int mask)
 {
     return mask_is_causal(mask) ? (num_qblocks + 1) / 2 : num_qblocks;
@@ -146,7 +156,7 @@ __device__ __forceinline__ int tiles_of_unit(int u, const FwdParams& p)
 }
 
 template <int MASK, bool SHARED>
-__device__ __forceinline__ Unit tile_of(int u, int i, const FwdParams& p)
+__device__ __forceinline__ Unit unit_tile(int u, int i, const FwdParams& p)
 {
     Unit w;
     const int uph = SHARED ? p.num_qblocks : units_per_head(p.num_qblocks, MASK);
@@ -166,20 +176,116 @@ __device__ __forceinline__ Unit tile_of(int u, int i, const FwdParams& p)
         const int last = min(w.q0 + BM - 1, p.n - 1) + w.off;
         w.nkv = last < 0 ? 0 : min(last / BN + 1, w.nkv);
     }
+    w.j0 = 0;
+    w.whole = true;
     return w;
 }
 
-// Position in this CTA's sequence of tiles: unit u, tile ti of that unit.
+// Position in this CTA's sequence of tiles: unit u, query tile ti of that unit. With shares:
+// unit u, its key tile ti, key tiles left of the share.
 struct TilePos {
-    int u, ti;
+    int u, ti, left;
 };
+
+constexpr int START = SHARE_START;
+
+template <int MASK, bool SHARED>
+__device__ __forceinline__ Unit tile_of(const TilePos& t, const FwdParams& p)
+{
+    if (!SHARED || p.ctas == 0) return unit_tile<MASK, SHARED>(t.u, t.ti, p);
+    Unit w = unit_tile<MASK, SHARED>(t.u, 0, p);
+    const int rest = min(w.nkv - t.ti, t.left);
+    w.whole = rest == w.nkv;
+    w.j0 = t.ti;
+    w.nkv = rest;
+    return w;
+}
+
+template <bool SHARED>
+__device__ __forceinline__ bool more(const TilePos& t, const FwdParams& p)
+{
+    return SHARED && p.ctas > 0 ? t.left > 0 : t.u < p.num_units;
+}
 
 template <int MASK, bool SHARED>
 __device__ __forceinline__ void advance(TilePos& t, int u_step, const FwdParams& p)
 {
+    if (SHARED && p.ctas > 0) {
+        t.left -= max(tile_of<MASK, SHARED>(t, p).nkv, 1) + START;
+        t.ti = 0;
+        ++t.u;
+        return;
+    }
     if (++t.ti >= tiles_of_unit<MASK, SHARED>(t.u, p)) {
         t.ti = 0;
         t.u += u_step;
+    }
+}
+
+// This CTA's share of the key tiles (p.ctas > 0), by one warp: where it begins, its length, the tiles
+// per share. (The host sees to it that the tiles of all units are fewer than 2^31.)
+constexpr int MIN_SHARE = 4;
+
+template <int MASK>
+__device__ __forceinline__ void first_of_share(const FwdParams& p, int lane, TilePos* first, int* length, int* per_cta)
+{
+    struct Entry {
+        int nkv, off, n;
+        __device__ int cost(int qb) const
+        {
+            if (!mask_is_causal(MASK)) return START + max(nkv, 1);
+            const int last = min(qb * BM + BM, n) - 1 + off;
+            return START + (last < 0 ? 1 : max(min(last / BN + 1, nkv), 1));
+        }
+    };
+    auto entry = [&](int b) {
+        int len = p.m;
+        if (mask_has_lengths(MASK)) len = min(max(__ldg(p.key_lengths + b), 0), p.m);
+        return Entry{(len + BN - 1) / BN, causal_offset(MASK, p.causal_off, len, p.n), p.n};
+    };
+    auto entry_cost = [&](int b) {                      // of all its units
+        if (b >= p.B) return 0;
+        const Entry e = entry(b);
+        int sum = 0;
+        for (int qb = 0; qb < p.num_qblocks; ++qb) sum += e.cost(qb);
+        return sum * p.H;
+    };
+    const int first32 = entry_cost(lane);
+    int total = first32;
+    for (int b = lane + 32; b < p.B; b += 32) total += entry_cost(b);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+    const int each = max((total - 1) / p.ctas + 1, MIN_SHARE);
+    const int64_t begin = static_cast<int64_t>(each) * blockIdx.x;
+    *per_cta = each;
+    *first = TilePos{0, 0, begin < total ? min(each, total - static_cast<int>(begin)) : 0};
+    *length = first->left;
+    if (first->left == 0) return;
+    int rest = static_cast<int>(begin);
+    for (int base = 0; base < p.B; base += 32) {
+        const int mine = base == 0 ? first32 : entry_cost(base + lane);
+        int upto = mine;                                 // inclusive prefix
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += x;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, upto > rest);
+        if (past != 0) {
+            const int l = __ffs(past) - 1, b = base + l;
+            rest -= __shfl_sync(0xffffffffu, upto - mine, l);
+            const int per_head = __shfl_sync(0xffffffffu, mine, l) / p.H;
+            const int h = rest / per_head;
+            rest -= h * per_head;
+            const Entry e = entry(b);
+            int qb = 0;
+            for (int c = e.cost(0); rest >= c; c = e.cost(++qb)) rest -= c;
+            first->u = (b * p.H + h) * p.num_qblocks + qb;
+            first->ti = max(rest - START, 0);
+            first->left -= max(START - rest, 0);
+            return;
+        }
+        rest -= __shfl_sync(0xffffffffu, upto, 31);
     }
 }
 
@@ -203,7 +309,7 @@ attn_fwd_dp_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     const int lane = threadIdx.x % 32;
     const uint64_t limit = p.watchdog_ns;
     const int u_step = static_cast<int>(gridDim.x);
-    const TilePos first_tile{static_cast<int>(blockIdx.x), 0};
+    TilePos first_tile{static_cast<int>(blockIdx.x), 0, 0};
 
     if (threadIdx.x == 0) {
         mbar_init(bar(L::B_QFULL), 1);
@@ -247,6 +353,25 @@ attn_fwd_dp_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     // unit, measured slower than the implicit one at this grid's completion.)
     griddep_wait();
 
+    int* const share = reinterpret_cast<int*>(smem + L::MISC_OFF + 8);   // the share's length, tiles per share
+    if (SHARED && p.ctas > 0) {
+        int* const slot = reinterpret_cast<int*>(smem + L::OST_OFF);     // (free until the first epilogue)
+        if (warp == 0) {
+            int length, per_cta;
+            first_of_share<MASK>(p, lane, &first_tile, &length, &per_cta);
+            if (lane == 0) {
+                slot[0] = first_tile.u;
+                slot[1] = first_tile.ti;
+                slot[2] = first_tile.left;
+                share[0] = length;
+                share[1] = per_cta;
+            }
+        }
+        __syncthreads();
+        first_tile = TilePos{slot[0], slot[1], slot[2]};
+        __syncthreads();
+    }
+
     const uint32_t sQ = sbase + L::Q_OFF;
     const uint32_t sK = sbase + L::K_OFF;
     const uint32_t sV = sbase + L::V_OFF;
@@ -285,8 +410,8 @@ attn_fwd_dp_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 ++vc;
                 return true;
             };
-            for (TilePos t = first_tile; ok && t.u < p.num_units; advance<MASK, SHARED>(t, u_step, p)) {
-                const Unit w = tile_of<MASK, SHARED>(t.u, t.ti, p);
+            for (TilePos t = first_tile; ok && more<SHARED>(t, p); advance<MASK, SHARED>(t, u_step, p)) {
+                const Unit w = tile_of<MASK, SHARED>(t, p);
                 if (w.nkv == 0) continue;
                 // the previous tile's Q must have left the buffer
                 if (qc > 0 && !mbar_wait_suspend(bar(L::B_QFREE), static_cast<uint32_t>(qc - 1) & 1u, abort_word,
@@ -300,10 +425,10 @@ attn_fwd_dp_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 ++qc;
                 // K(j+1) is issued before V(j): S(j+1) needs it while P(j) is computed
                 const int kv = SHARED ? w.bh / p.kv_group : w.bh;
-                ok = load_K(kv, 0);
+                ok = load_K(kv, w.j0);
                 for (int j = 0; ok && j < w.nkv; ++j) {
-                    if (j + 1 < w.nkv) ok = load_K(kv, j + 1);
-                    if (ok) ok = load_V(kv, j);
+                    if (j + 1 < w.nkv) ok = load_K(kv, w.j0 + j + 1);
+                    if (ok) ok = load_V(kv, w.j0 + j);
                 }
             }
             // land every copy still in flight (only possible after an abort)
@@ -362,8 +487,8 @@ attn_fwd_dp_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 ++g;
                 return true;
             };
-            for (TilePos t = first_tile; ok && t.u < p.num_units; advance<MASK, SHARED>(t, u_step, p)) {
-                const Unit w = tile_of<MASK, SHARED>(t.u, t.ti, p);
+            for (TilePos t = first_tile; ok && more<SHARED>(t, p); advance<MASK, SHARED>(t, u_step, p)) {
+                const Unit w = tile_of<MASK, SHARED>(t, p);
                 if (w.nkv == 0) continue;
                 ok = wait(L::Q_IN_TMEM ? L::B_QREADY : L::B_QFULL, static_cast<uint32_t>(qc) & 1u);
                 ++qc;
@@ -401,7 +526,7 @@ attn_fwd_dp_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         bool ok = true;
         int g = 0;        // key-tile steps over all tiles
         int qc = 0;       // tiles whose Q went into tensor memory
-        TilePos q_done{-1, 0};   // last tile whose Q was copied
+        TilePos q_done{-1, 0, 0};   // last tile whose Q was copied
         bool store_pending = false;
 
         if (p.debug_flags & DEBUG_FORCE_TIMEOUT) {
@@ -439,8 +564,8 @@ attn_fwd_dp_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             return true;
         };
 
-        for (TilePos t = first_tile; ok && t.u < p.num_units; advance<MASK, SHARED>(t, u_step, p)) {
-            const Unit w = tile_of<MASK, SHARED>(t.u, t.ti, p);
+        for (TilePos t = first_tile; ok && more<SHARED>(t, p); advance<MASK, SHARED>(t, u_step, p)) {
+            const Unit w = tile_of<MASK, SHARED>(t, p);
             const int qrow = w.q0 + r;
             const int qlim = qrow + w.off;   // the row's key position: last key it sees under the causal mask
             // distance-bias slope of the head, log2 domain
@@ -473,7 +598,7 @@ attn_fwd_dp_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 #pragma unroll
                 for (int c = 0; c < BN; ++c) s[c] = __uint_as_float(sr[c]);
                 uint32_t pk[BN / 2];
-                const float alpha = smx::tile_step<MASK, BIAS>(s, j * BN, w.kv_len, qlim, sl2, sb, m_ref, l_run, pk);
+                const float alpha = smx::tile_step<MASK, BIAS>(s, (w.j0 + j) * BN, w.kv_len, qlim, sl2, sb, m_ref, l_run, pk);
 
                 if (g > 0) {
                     // the previous O += P V must be complete: it reads the P columns,
@@ -517,13 +642,52 @@ attn_fwd_dp_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 // previous tile is complete, so the Q buffer being overwritten is free)
                 TilePos nt = t;
                 advance<MASK, SHARED>(nt, u_step, p);
-                while (nt.u < p.num_units && tile_of<MASK, SHARED>(nt.u, nt.ti, p).nkv == 0) advance<MASK, SHARED>(nt, u_step, p);
+                while (more<SHARED>(nt, p) && tile_of<MASK, SHARED>(nt, p).nkv == 0) advance<MASK, SHARED>(nt, u_step, p);
                 // (a tile without keys between two with keys finds its successor's Q
                 // already copied by the tile before it)
-                if (nt.u < p.num_units && !(q_done.u == nt.u && q_done.ti == nt.ti)) {
+                if (more<SHARED>(nt, p) && !(q_done.u == nt.u && q_done.ti == nt.ti)) {
                     ok = copy_q();
                     if (!ok) break;
                     q_done = nt;
+                }
+            }
+            if (SHARED && p.ctas > 0) {
+                if (r == 0 && t.ti == 0) {               // which CTAs have tiles of this unit
+                    const int tiles = max(unit_tile<MASK, SHARED>(t.u, 0, p).nkv, 1);
+                    const int c = static_cast<int>(blockIdx.x);
+                    p.unit_parts[t.u] = make_int2(c, c + (share[0] - t.left + tiles - 1) / share[1]);
+                }
+                if (!w.whole) {
+                    // a part: O as it stands leaves through the staging tile, 32 rows x 32 columns (4 KB) at a
+                    // time. (Stored by the threads, 64 KB held up the next tile's hand-over by 3 us.)
+                    const int slot = 2 * static_cast<int>(blockIdx.x) + (t.ti > 0 ? 0 : 1);
+                    p.part_ml[slot * BM + r] = make_float2(m_ref, l_run);
+                    float* const dst = p.part_o + static_cast<int64_t>(slot) * (BM * DV) + warp * (32 * DV);
+#pragma unroll
+                    for (int cc = 0; cc < DV / 32; ++cc) {
+                        const uint32_t area = sO + (cc % L::CHV) * CHUNK_BYTES + warp * 4096;
+                        if (cc % L::CHV == 0) {
+                            if (store_pending && lane == 0) bulk_wait_group_read0();
+                            __syncwarp();
+                        }
+                        uint32_t o[32];
+                        tmem_ld32(tO + 32 * cc, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(area + q * 512 + lane * 16),
+                                         "r"(o[4 * q]), "r"(o[4 * q + 1]), "r"(o[4 * q + 2]), "r"(o[4 * q + 3])
+                                         : "memory");
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            bulk_store(dst + cc * 1024, area, 4096);
+                            bulk_commit_group();
+                        }
+                        store_pending = true;
+                    }
+                    __syncwarp();
+                    continue;
                 }
             }
             const bool any = l_run > 0.f;
@@ -582,6 +746,66 @@ attn_fwd_dp_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     }
 }
 
+// Joins the parts of the cut units: O = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k. A CTA
+// takes 16 columns of a unit, a thread one row of them; the parts come mostly out of L2, whose
+// latency bounds this, so several are asked for at a time.
+template <int DV>
+__global__ void __launch_bounds__(BM) attn_fwd_merge_kernel(const FwdParams p)
+{
+    constexpr int AT_ONCE = 4;
+    griddep_wait();
+    const int u = blockIdx.x, r = threadIdx.x;
+    const int2 span = p.unit_parts[u];
+    // whole units; and, after a wait that gave up, a span that was never written
+    if (span.x < 0 || span.y <= span.x || span.y >= p.ctas) return;
+    const int64_t bh = u / p.num_qblocks;
+    const int qrow = u % p.num_qblocks * BM + r;
+    if (qrow >= p.n) return;
+    auto slot_of = [&](int c) { return 2 * c + (c == span.x ? 1 : 0); };
+    float M = -INFINITY;
+#pragma unroll 8
+    for (int c = span.x; c <= span.y; ++c) M = fmaxf(M, p.part_ml[slot_of(c) * BM + r].x);
+    const float M_use = M == -INFINITY ? 0.f : M;
+    float acc[16] = {}, l = 0.f;
+    for (int c0 = span.x; c0 <= span.y; c0 += AT_ONCE) {
+        float2 ml[AT_ONCE];
+        float4 x[AT_ONCE][4];
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) {
+            const int slot = slot_of(min(c0 + i, span.y));
+            ml[i] = p.part_ml[slot * BM + r];
+            const float4* const src = reinterpret_cast<const float4*>(p.part_o) + static_cast<int64_t>(slot) * (BM * DV / 4) +
+                                      r / 32 * (8 * DV) + blockIdx.y * 128 + r % 32;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) x[i][q] = src[q * 32];
+        }
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) {
+            if (c0 + i > span.y || (ml[i].x == -INFINITY && ml[i].y == 0.f)) continue;   // the row sees nothing of it
+            const float f = ex2_approx(ml[i].x - M_use);
+            l = fmaf(ml[i].y, f, l);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                acc[4 * q] = fmaf(x[i][q].x, f, acc[4 * q]);
+                acc[4 * q + 1] = fmaf(x[i][q].y, f, acc[4 * q + 1]);
+                acc[4 * q + 2] = fmaf(x[i][q].z, f, acc[4 * q + 2]);
+                acc[4 * q + 3] = fmaf(x[i][q].w, f, acc[4 * q + 3]);
+            }
+        }
+    }
+    const bool any = l > 0.f;
+    const float inv_l = any ? 1.f / l : 0.f;
+    const int64_t row = bh * p.n + qrow;
+    if (blockIdx.y == 0 && p.LSE != nullptr) p.LSE[row] = any ? (M_use + __log2f(l)) * LN2 : -INFINITY;
+    uint4* const out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.O) + row * DV + 16 * blockIdx.y);
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+        out[q] = make_uint4(pack_bf16x2(acc[8 * q] * inv_l, acc[8 * q + 1] * inv_l),
+                            pack_bf16x2(acc[8 * q + 2] * inv_l, acc[8 * q + 3] * inv_l),
+                            pack_bf16x2(acc[8 * q + 4] * inv_l, acc[8 * q + 5] * inv_l),
+                            pack_bf16x2(acc[8 * q + 6] * inv_l, acc[8 * q + 7] * inv_l));
+}
+
 template <int DK, int DV, int MASK, bool BIAS = false, bool SHARED = false>
 cudaError_t launch(const TensorMaps& maps, const FwdParams& p, int num_sms, cudaStream_t stream)
 {
@@ -598,6 +822,17 @@ cudaError_t launch(const TensorMaps& maps, const FwdParams& p, int num_sms, cuda
         configured[dev] = true;
     }
     const int64_t slots = static_cast<int64_t>(num_sms) * L::CTAS_PER_SM;
+    if constexpr (SHARED) {
+        if (p.ctas > 0) {
+            FwdParams q = p;
+            q.ctas = static_cast<int>(p.ctas < slots ? p.ctas : slots);
+            e = launch_pdl(kern, dim3(static_cast<unsigned>(q.ctas)), dim3(L::NUM_THREADS), L::BYTES, stream, maps.q, maps.k,
+                           maps.v, maps.o, q);
+            if (e != cudaSuccess) return e;
+            return launch_pdl(attn_fwd_merge_kernel<DV>, dim3(static_cast<unsigned>(p.num_units), DV / 16), dim3(BM), 0,
+                              stream, q);
+        }
+    }
     const int64_t grid = p.num_units < slots ? p.num_units : slots;
     return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(L::NUM_THREADS), L::BYTES, stream, maps.q,
                       maps.k, maps.v, maps.o, p);
