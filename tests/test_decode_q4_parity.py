@@ -12,7 +12,8 @@ times the bf16 value) are exact in the kernels. With w the softmax weights, v = 
   - A score is scale sum_c q_c s (u_c - u0) in fp32: per group four tensor-core additions of
     q u, the zero taken out, the step, then the sum of the groups and the scale, at most 14
     roundings of up to 2^-23 of sum_c |q_c| s u_c (or of what u0 takes out, no larger than s 15);
-    the distance bias adds one of its own size. With G = scale max (sum_c |q_c| s 15) + max bias:
+    the distance bias adds one of its own size. (Products of a q below 2^-7 of the row's largest also lose
+    what is below 2^-14 of that largest; of normal q that is one or two in 64, inside the 14.) With G = scale max (sum_c |q_c| s 15) + max bias:
     e = 14 2^-23 G. A weight then moves by e w and the sum of the weights too: O by 2 e A, A = sum_j w_j |v_j|.
   - O is rounded to bf16: 2^-8 of what was rounded.
 
@@ -230,6 +231,19 @@ def test_rows_with_a_zero_query_take_the_mean():
     c.check("zero queries")
     _, L = c.run()
     assert np.abs(L - np.log(777)).max() <= 1e-5
+
+
+@pytest.mark.parametrize("dk", [64, 128])
+def test_lse_of_few_slots(dk):
+    """LSE at the size of single scores, where nothing averages out: off by a few units of fp32
+    (2^-23) of the scores and of what u0 takes out, which has about their size: 2^-20 rms."""
+    for m in (1, 4):
+        K, V = (torch.randn((8, 16, m, d), generator=torch.Generator().manual_seed(m)).to(torch.bfloat16) for d in (dk, 64))
+        c = Case(8, 16, 1, 1, m, dk, 64, "none", seed=40 + m, K=K, V=V)
+        _, L = c.run()
+        Lr = oracle.attn_fwd(c.Q, c.K, c.V, "none", None, None, threads=8)[1]
+        off = float(np.sqrt(np.mean((L - Lr) ** 2)) / np.sqrt(np.mean(Lr ** 2)))
+        assert off <= 2.0 ** -20, f"m={m}: {off:.2e}"
 
 
 def test_scale():
