@@ -355,7 +355,7 @@ int attn_merge_proj(const void* O, const void* W_o, const void* bias, int B, int
  *   the query tiles alone would not fill the SMs. The first call on a device allocates a status
  *   word: make one before a stream capture. The workspace (caller-owned, 256-byte aligned, at
  *   least attn_decode_q4_workspace_size(...) bytes, contents on entry do not matter; 0
- *   for short caches) belongs to one call at a time: calls that may overlap need one
+ *   for few or short caches) belongs to one call at a time: calls that may overlap need one
  *   each. O and LSE do not depend on the order in which CTAs run.
  * All run on `stream` without synchronising. Return ATTN_OK or a negative
  * attn_status_t (INVALID_ARG: H not a multiple of H_kv, a slot range outside the cache, a

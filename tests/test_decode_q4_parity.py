@@ -119,7 +119,7 @@ class Case:
 
 
 @pytest.mark.parametrize("dk,dv", DIMS)
-@pytest.mark.parametrize("m", [1, 15, 64, 65, 700, 1025, 4097])
+@pytest.mark.parametrize("m", [1, 15, 64, 65, 700, 1025, 4097, 12345])
 def test_one_token(dk, dv, m):
     Case(2, 3, 1, 1, m, dk, dv, seed=m).check(f"m={m}")
 
@@ -128,14 +128,14 @@ def test_one_token(dk, dv, m):
 @pytest.mark.parametrize("group,n", [(1, 2), (1, 8), (2, 4), (3, 3), (8, 1), (5, 3), (16, 1), (4, 7), (8, 8)])
 def test_rows_that_share_a_cache_head(dk, dv, group, n):
     """2 to 64 rows per cache head: one and several row tiles, whole and partial."""
-    for m in (200, 2000):
+    for m in (200, 2000, 9000):
         Case(2, 2, group, n, m, dk, dv, "causal", seed=group * n + m).check(f"group={group} n={n} m={m}")
 
 
 @pytest.mark.parametrize("dk,dv", DIMS)
 @pytest.mark.parametrize("mask", MASKS)
 @pytest.mark.parametrize("n", [1, 5])
-@pytest.mark.parametrize("m", [300, 1500])
+@pytest.mark.parametrize("m", [300, 1500, 9000])
 def test_masks_and_lengths(dk, dv, mask, n, m):
     """Lengths full, 0, 1, fewer than the rows, on and next to a block's end."""
     lens = [m, 0, 1, 3, 64, 65, 127, 128, m - 1] if mask in inputs.LENGTH_MASKS else None
@@ -143,7 +143,7 @@ def test_masks_and_lengths(dk, dv, mask, n, m):
 
 
 @pytest.mark.parametrize("mask", MASKS)
-@pytest.mark.parametrize("m", [130, 1300])
+@pytest.mark.parametrize("m", [130, 1300, 9001])
 def test_distance_bias(mask, m):
     lens = [m, 0, 70, 5] if mask in inputs.LENGTH_MASKS else None
     Case(4, 2, 3, 3, m, 64, 128, mask, lens, seed=m, slopes=True).check(f"{mask} m={m}")
@@ -212,10 +212,11 @@ def test_a_row_that_sees_only_small_values_next_to_large_ones():
 
 @pytest.mark.parametrize("dk,dv", DIMS)
 @pytest.mark.parametrize("B,H_kv,group,n,m", [
-    (4, 2, 1, 1, 128), (38, 8, 1, 1, 130), (61, 5, 1, 1, 130), (2, 3, 5, 2, 705), (2, 3, 5, 2, 769), (3, 1, 12, 4, 768)])
+    (4, 2, 1, 1, 128), (38, 8, 1, 1, 130), (61, 5, 1, 1, 130), (2, 3, 5, 2, 705), (19, 8, 1, 1, 769), (3, 1, 12, 4, 768),
+    (19, 4, 1, 1, 1030), (2, 2, 3, 3, 1030), (19, 2, 1, 2, 3333), (38, 8, 1, 1, 1025), (1, 1, 1, 1, 8192), (1, 1, 1, 1, 8193)])
 def test_short_caches(dk, dv, B, H_kv, group, n, m):
-    """2 to 13 blocks per pair, 6 to 305 pairs: the pairs that get a CTA each and the next ones that
-    do not; lengths that leave some of a CTA's warps, or all of them, without a block."""
+    """The pairs that get a CTA or a cluster of 2, 4 or 8 each, and the next ones that do not (305 pairs,
+    17 blocks for 304, 129 blocks); lengths that leave some of a CTA's warps, or all of them, without a block."""
     lens = [(m - b * 67) % (m + 1) if b % 4 != 3 else b % 3 * 64 for b in range(B)]
     Case(B, H_kv, group, n, m, dk, dv, "causal_cache", lens, seed=B + m).check(f"B={B} m={m}")
 
@@ -251,8 +252,8 @@ def test_scale():
 
 
 def test_a_slot_that_cannot_be_held_reaches_every_row_that_sees_it():
-    """Early, in a cut pair's first part, in a CTA's second warp: NaN survives each kind of merge."""
-    for m, at in ((60, 3), (700, 300), (9000, 5), (9000, 8999)):
+    """Early, in a cut pair's parts, in a CTA's second warp, in a cluster: NaN survives each kind of merge."""
+    for m, at in ((60, 3), (400, 300), (700, 300), (4000, 3000), (9000, 5), (9000, 8999)):
         V = rows(12, (1, 2, m, 128))
         K = rows(11, (1, 2, m, 64))
         V[0, 0, at, 77] = float("nan")
@@ -295,14 +296,15 @@ def test_the_same_call_gives_the_same_bits():
     assert np.array_equal(O, O2) and np.array_equal(L, L2)
 
 
-def test_decoding_run_through_a_captured_graph():
+@pytest.mark.parametrize("m", [1200, 9100])
+def test_decoding_run_through_a_captured_graph(m):
     """Tokens written one by one and attended to, lengths advancing on the device: each
     step equals the oracle on what the cache then holds, and an eager call's bits."""
-    B, H_kv, group, m, steps = 3, 2, 2, 1200, 40
+    B, H_kv, group, steps = 3, 2, 2, 40
     K, V = rows(16, (B, H_kv, m, 128)), rows(17, (B, H_kv, m, 128))
     g = torch.Generator().manual_seed(18)
     Qs = torch.randn(steps, B, H_kv * group, 1, 128, generator=g).to(torch.bfloat16)
-    first = [0, 63, 1100]
+    first = [0, 63, m - 100]
     cache = torch.full((B, H_kv, -(-m // 64), 34 * 256), 0xFF, dtype=torch.uint8, device="cuda")
     attn.cache_q4_write(cache, K.cuda(), V.cuda(), None, i32(first), m=m)
     lens = i32(first)
@@ -353,10 +355,11 @@ def test_agrees_with_the_forward_on_the_cache_read_back():
 
 def test_two_calls_at_once():
     """A stream each with a workspace of its own, many times over: the bits of a lone call."""
-    cases = [Case(3, 4, 2, 3, 5000, 128, 128, "causal_cache", [5000, 1, 3333], seed=30),
+    cases = [Case(3, 4, 2, 3, 9000, 128, 128, "causal_cache", [9000, 1, 3333], seed=30),
              Case(4, 2, 4, 1, 7000, 128, 128, "key_padding", [7000, 0, 128, 6001], seed=31),
              Case(2, 2, 2, 90, 4500, 128, 64, "causal_cache", [4500, 2077], seed=37),
-             Case(3, 2, 2, 1, 600, 128, 128, "key_padding", [600, 64, 300], seed=38)]
+             Case(3, 2, 2, 1, 500, 128, 128, "key_padding", [500, 64, 300], seed=38),
+             Case(3, 2, 2, 1, 3000, 128, 128, "key_padding", [3000, 64, 300], seed=39)]
     want = [c.run() for c in cases]
     streams = [torch.cuda.Stream() for _ in cases]
     Q = [c.Q.cuda() for c in cases]
@@ -422,8 +425,8 @@ def test_no_slots_and_no_rows():
 def test_forced_timeout_reports_and_recovers():
     """The bounded wait of the kernel's warps gives up, the status reports it, and a
     normal call afterwards is right."""
-    # shares of all blocks; a CTA per pair; many rows in shares of the key tiles
-    for m, n in ((4096, 1), (700, 1), (4096, 100)):
+    # shares of all blocks; a cluster and a CTA per pair; many rows in shares of the key tiles
+    for m, n in ((9000, 1), (4096, 1), (400, 1), (4096, 100)):
         c = Case(2, 2, 1, n, m, 128, 128, "none", seed=20)
         attn.set_watchdog(0, 1)
         try:

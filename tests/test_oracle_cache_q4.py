@@ -148,7 +148,7 @@ def test_read_refusals(lib, kw, code):
     (dict(n=0), attn.ATTN_OK), (dict(B=0), attn.ATTN_OK),
 ])
 def test_decode_refusals(lib, kw, code):
-    a = dict(Q=P, cache=P, B=1, H=4, Hk=2, n=1, m=8192, dk=64, dv=64, mask=0, lens=None, slopes=None, O=P2, LSE=None,
+    a = dict(Q=P, cache=P, B=1, H=4, Hk=2, n=1, m=16384, dk=64, dv=64, mask=0, lens=None, slopes=None, O=P2, LSE=None,
              ws=P, ws_bytes=1 << 30)
     a.update(kw)
     assert lib.attn_decode_q4(a["Q"], a["cache"], a["B"], a["H"], a["Hk"], a["n"], a["m"], a["dk"], a["dv"], a["mask"],
@@ -163,6 +163,11 @@ def test_sizes(lib):
     # 17/64 of the bf16 cache
     assert lib.attn_cache_q4_size(64, 16, 8192, 128, 128) * 64 == 64 * 16 * 8192 * 512 * 17
     assert attn.decode_q4_workspace_size(8, 8, 8, 1, 64, 64, 64) == 0
+    # a pair to a CTA or a cluster, up to 16 blocks to a CTA: none
+    assert attn.decode_q4_workspace_size(1, 8, 8, 1, 8192, 64, 64) == 0
+    assert attn.decode_q4_workspace_size(1, 8, 8, 1, 8193, 64, 64) > 0
+    assert attn.decode_q4_workspace_size(38, 8, 8, 1, 1024, 64, 64) == 0
+    assert attn.decode_q4_workspace_size(38, 8, 8, 1, 1025, 64, 64) > 0
     # many rows: the cache as bf16
     assert attn.decode_q4_workspace_size(256, 8, 4, 100, 4096, 128, 64) == 256 * 4 * 4096 * 192 * 2
     # few rows: bounded however large the batch and the cache are

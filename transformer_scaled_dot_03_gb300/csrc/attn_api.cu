@@ -982,12 +982,16 @@ namespace {
 
 constexpr int kQ4MaxRows = 64;            // rows per cache head up to which the few-row kernel runs
 constexpr int kQ4WholeBlocks = 2;         // up to this many blocks per (b, cache head) a warp takes whole pairs
-// Two to kQ4CtaBlocks blocks and at most kQ4CtaPairs pairs (the CTA slots of 152 SMs): a CTA per
-// pair. B x 8 heads, lengths m/2..m, us with a CTA per pair and with shares (one launch more):
-// 64/64, B = 16: m 256 3.6 / 7.4, m 512 4.6 / 7.2; B = 32: m 512 5.4 / 8.5; 128/128, B = 8:
-// m 512 6.2 / 8.1, m 1024 8.9 / 8.5, m 1536 12.2 / 9.7; 512 pairs: m 128 6.7 / 4.8, m 512 10.0 / 10.5.
-constexpr int kQ4CtaBlocks = 12;
-constexpr int64_t kQ4CtaPairs = 304;
+// Few short pairs: a CTA per pair up to kQ4OneCta blocks, from there on a cluster of up to eight
+// that gives each warp one block, as far as all of them fit into the CTA slots of 152 SMs and the
+// blocks are at most kQ4CtaBlocks per CTA. B x 8 heads, lengths m/2..m, us with one CTA, with a
+// cluster, and with shares and the second launch for their parts: 64/64, B = 4: m 256 3.6 / - / 7.2,
+// m 512 4.6 / 5.1 (2) / 6.8, m 1024 6.8 / 5.2 (4) / 7.0, m 4096 - / 6.7 (8) / 8.5, m 8192 - / 9.1 (8) / 10.4;
+// 128/128: B = 4, m 1024 - / 6.7 (4) / 8.1, B = 8, m 4096 - / 12.4 (4) / 12.6, m 8192 - / 18.8 (4: 32
+// blocks per CTA) / 16.8; B = 32, m 1024 11.0 / - / 12.1; B = 64, m 512 (512 pairs) 13.3 / - / 13.2.
+constexpr int kQ4OneCta = 8;
+constexpr int kQ4CtaBlocks = 16;
+constexpr int64_t kQ4CtaSlots = 304;
 // Many rows: whole query tiles go round the CTAs in ceil(units / CTAs) turns of up to `tiles` key
 // tiles; equal shares take units (tiles + SHARE_START) / CTAs and kQ4ShareCost tiles' time more (the
 // parts' way to memory, the kernel that joins them). 16 heads, lengths m/2..m, 128/128, us in
@@ -1013,7 +1017,7 @@ int q4_blocks(int m) { return static_cast<int>((static_cast<int64_t>(m) + attn::
 // Scratch of attn_decode_q4: the parts of split pairs, or for many rows K and V as bf16.
 struct Q4Plan {
     bool few;
-    int mode;                         // few: attn::Q4_*
+    int mode, cluster;                // few: attn::Q4_*; CTAs per pair (Q4_CTA)
     int rows, row_tiles;              // rows per cache head, tiles of them
     int64_t pairs, warps;             // (b, cache head, row tile) triples; most workers
     int part_rows;
@@ -1048,9 +1052,12 @@ Q4Plan q4_plan(int64_t B, int64_t H, int64_t H_kv, int64_t n, int m, int d_k, in
     w.row_tiles = (w.rows + tile - 1) / tile;
     w.pairs = B * H_kv * w.row_tiles;
     const int64_t blocks = q4_blocks(m);
-    w.mode = blocks > 1 && blocks <= kQ4CtaBlocks && w.pairs <= kQ4CtaPairs ? attn::Q4_CTA
-             : blocks <= kQ4WholeBlocks                                     ? attn::Q4_WHOLE
-                                                                            : attn::Q4_SHARES;
+    w.cluster = 1;
+    while (w.cluster < 8 && blocks > (w.cluster == 1 ? kQ4OneCta : 4 * w.cluster) && w.pairs * w.cluster * 2 <= kQ4CtaSlots)
+        w.cluster *= 2;
+    w.mode = blocks > 1 && blocks <= kQ4CtaBlocks * w.cluster && w.pairs * w.cluster <= kQ4CtaSlots ? attn::Q4_CTA
+             : blocks <= kQ4WholeBlocks                                                             ? attn::Q4_WHOLE
+                                                                                                    : attn::Q4_SHARES;
     w.warps = std::min(q4_max_warps(tile), w.mode == attn::Q4_SHARES ? w.pairs * blocks : w.pairs);
     if (w.mode != attn::Q4_SHARES) return w;
     w.part_rows = std::min(w.rows, tile);
@@ -1217,6 +1224,7 @@ extern "C" int attn_decode_q4(const void* Q, const void* cache, int B, int H, in
     p.slopes = slopes;
     p.scale_log2 = static_cast<float>(sc * 1.4426950408889634074);
     p.mode = w.mode;
+    p.cluster = w.cluster;
     int num_sms = 0;
     if ((rc = sm_count(&num_sms)) != ATTN_OK) return rc;
     p.warps = static_cast<int>(std::min<int64_t>(

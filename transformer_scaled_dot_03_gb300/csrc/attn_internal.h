@@ -83,6 +83,27 @@ inline cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, siz
     return cudaLaunchKernelEx(&cfg, kern, static_cast<Args&&>(args)...);
 }
 
+// The same with clusters of `cluster` CTAs.
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_pdl_cluster(void (*kern)(KArgs...), int cluster, dim3 grid, dim3 block, size_t smem,
+                                      cudaStream_t stream, Args&&... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<Args&&>(args)...);
+}
+
 // Backward (attn_kernel_bwd.cuh): one CTA per (b, h, 128-key tile).
 struct BwdParams {
     int B, H, n, m;
@@ -201,7 +222,7 @@ cudaError_t launch_cache_q4_read(const CacheQ4ReadParams& p, cudaStream_t stream
 
 // Few-row attention over that cache (attn_kernel_decode_q4.cuh). How the (entry, cache
 // head, row tile) pairs are divided: equal shares of all blocks per warp, with parts merged by a
-// second kernel; whole pairs per warp; or a CTA per pair.
+// second kernel; whole pairs per warp; or a CTA, or a cluster of them, per pair.
 enum { Q4_SHARES = 0, Q4_WHOLE = 1, Q4_CTA = 2 };
 
 struct DecodeQ4Params {
@@ -217,6 +238,7 @@ struct DecodeQ4Params {
     float scale_log2;             // scale * log2(e)
     int mode;                     // Q4_*
     int warps;                    // workers (Q4_SHARES, Q4_WHOLE)
+    int cluster;                  // CTAs per pair (Q4_CTA): 1, 2, 4 or 8
     uint16_t* O;                  // bf16 [B,H,n,d_v]
     float* LSE;                   // fp32 [B,H,n] or null
     float* part_o;                // fp32 [2 warps][part_rows][d_v] (Q4_SHARES)

@@ -52,10 +52,11 @@
 // order. (Chunks that an SM's warps take in turn cost more in pair starts than the
 // better balance gives.)
 //
-// Few short pairs (Q4_CTA) take a CTA each, whose warps divide the pair's blocks and merge
-// their parts in shared memory: one launch and no workspace. With more pairs than CTA slots
-// its latencies (6 us per pair) would not be covered, and short pairs then go whole to a
-// warp each (Q4_WHOLE).
+// Few short pairs (Q4_CTA) take a CTA or a cluster of CTAs each, whose warps divide the pair's blocks;
+// each CTA merges its warps' parts in its shared memory, then every CTA of the cluster some
+// columns of all the CTAs' parts through distributed shared memory: one launch and no workspace.
+// With more pairs than CTA slots its latencies (6 us per pair) would not be covered, and short pairs
+// then go whole to a warp each (Q4_WHOLE).
 //
 // Measured: 64 entries of 4096 to 8192 slots, 16 heads of 128 + 128 channels, one row: 140 us,
 // 6.1 TB/s of the 858 MB read, 90% of the copy rate. Without the products the copies alone take 130 us,
@@ -66,6 +67,7 @@
 
 #include <cstdint>
 #include <cuda_runtime.h>
+#include <type_traits>
 
 #include "attn_cache_q4.cuh"
 #include "attn_internal.h"
@@ -79,6 +81,7 @@ namespace dq4 {
 
 constexpr int WARPS = 4;
 constexpr int THREADS = 32 * WARPS;
+constexpr int MAX_CLUSTER = 8;
 constexpr float LN2 = 0.693147180559945309f;
 constexpr float LOG2E = 1.44269504088896341f;
 constexpr uint32_t LO = 0x000F000Fu, HI = 0x00F000F0u, ZERO = 0x03C003C0u;
@@ -91,7 +94,7 @@ struct Layout {
     // 2 blocks of 8704 or 6528 bytes, or 3 of 4352, in flight per warp
     static constexpr int STAGES = DK + DV == 128 ? 3 : 2;
     static constexpr int RING = WARPS * STAGES * BYTES_BLOCK;
-    static_assert(ROWS * (DV + 2) * 4 <= STAGES * BYTES_BLOCK, "a warp's part fits its ring");
+    static_assert(ROWS * (DV + 4) * 4 <= STAGES * BYTES_BLOCK, "a warp's part (and the CTA's sums) fit a ring");
     static constexpr int ROW_OFF = RING;                  // per warp and row: RowInfo
     static constexpr int BAR_OFF = ROW_OFF + WARPS * ROWS * 16;
     static constexpr int MISC_OFF = BAR_OFF + (WARPS * STAGES + 1) * 8;
@@ -317,12 +320,14 @@ attn_decode_q4_kernel(const DecodeQ4Params p)
     const int pairs_b = p.H_kv * p.row_tiles;            // pairs per entry
     Shares shares;
     Cursor at;
-    if constexpr (CTA) {                                 // a quarter of the CTA's pair
-        at.b = static_cast<int>(blockIdx.x) / pairs_b;
-        at.pr = static_cast<int>(blockIdx.x) - at.b * pairs_b;
+    if constexpr (CTA) {                                 // this warp's part of the cluster's pair
+        const int pair = static_cast<int>(blockIdx.x) / p.cluster, all = WARPS * p.cluster;
+        const int me = WARPS * (static_cast<int>(blockIdx.x) - pair * p.cluster) + warp;
+        at.b = pair / pairs_b;
+        at.pr = pair - at.b * pairs_b;
         at.nb = pair_blocks(p, at.b);
-        at.blk = at.nb * warp / WARPS;
-        at.todo = at.nb * (warp + 1) / WARPS - at.blk;
+        at.blk = at.nb * me / all;
+        at.todo = at.nb * (me + 1) / all - at.blk;
         at.before = 0;
         shares.each = shares.more = 0;
     } else {
@@ -816,36 +821,67 @@ attn_decode_q4_kernel(const DecodeQ4Params p)
     }
     if (!CTA) return;
 
-    // -------------------------------------------- Q4_CTA: merge the warps' parts
+    // -------------------------------------------- Q4_CTA: merge the warps' parts, then the CTAs'
     if (start.todo == 0 || !ok)                          // no part
         for (int r = lane; r < L::ROWS; r += 32) *reinterpret_cast<float2*>(own + 2 * r) = make_float2(-INFINITY, 0.f);
     __syncthreads();
     const int64_t pair_bh = static_cast<int64_t>(start.b) * p.H_kv + start.pr / p.row_tiles;
     const int r0 = start.pr % p.row_tiles * L::ROWS, rows = min(L::ROWS, p.R - r0);
-    for (int e = threadIdx.x; e < rows * (DV / 2); e += THREADS) {
-        const int row = e / (DV / 2), c = e % (DV / 2) * 2;
-        float2 ml[WARPS];
-        float M = -INFINITY, Lsum = 0.f, v0 = 0.f, v1 = 0.f;
+    // Two columns of a row from N parts: maximum and sum at ml(i), O at o(i)
+    auto merge = [&](auto n, auto&& load_ml, auto&& load_o, float* M, float* Lsum, float* v) {
+        float2 ml[decltype(n)::value], x[decltype(n)::value];
+        *M = -INFINITY;
+        *Lsum = v[0] = v[1] = 0.f;
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) {
-            ml[w] = *reinterpret_cast<const float2*>(smem + w * L::STAGES * L::BYTES_BLOCK + 8 * row);
-            M = fmaxf(M, ml[w].x);
+        for (int i = 0; i < decltype(n)::value; ++i) {
+            ml[i] = load_ml(i);
+            x[i] = load_o(i);
+            *M = fmaxf(*M, ml[i].x);
         }
-        const float M_use = M == -INFINITY ? 0.f : M;
+        const float M_use = *M == -INFINITY ? 0.f : *M;
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) {
-            if (ml[w].x == -INFINITY && ml[w].y == 0.f) continue;              // no part, or no visible slot in it
-            const float f = ex2_approx(ml[w].x - M_use);
-            const float2 x = *reinterpret_cast<const float2*>(smem + w * L::STAGES * L::BYTES_BLOCK + 8 * L::ROWS + 4 * (row * DV + c));
-            Lsum = fmaf(ml[w].y, f, Lsum);
-            v0 = fmaf(x.x, f, v0);
-            v1 = fmaf(x.y, f, v1);
+        for (int i = 0; i < decltype(n)::value; ++i) {
+            if (ml[i].x == -INFINITY && ml[i].y == 0.f) continue;              // no part, or no visible slot in it
+            const float f = ex2_approx(ml[i].x - M_use);
+            *Lsum = fmaf(ml[i].y, f, *Lsum);
+            v[0] = fmaf(x[i].x, f, v[0]);
+            v[1] = fmaf(x[i].y, f, v[1]);
         }
+    };
+    auto write = [&](int row, int c, float M, float Lsum, const float* v) {
         const int64_t orow = pair_bh * p.R + r0 + row;
         const float inv = Lsum == 0.f ? 0.f : 1.f / Lsum;                      // (a NaN sum is not 0: it reaches the output)
-        *reinterpret_cast<uint32_t*>(p.O + orow * DV + c) = pack_bf16x2(v0 * inv, v1 * inv);
-        if (c == 0 && p.LSE != nullptr) p.LSE[orow] = Lsum == 0.f ? -INFINITY : (M_use + __log2f(Lsum)) * LN2;
+        *reinterpret_cast<uint32_t*>(p.O + orow * DV + c) = pack_bf16x2(v[0] * inv, v[1] * inv);
+        if (c == 0 && p.LSE != nullptr)
+            p.LSE[orow] = Lsum == 0.f ? -INFINITY : ((M == -INFINITY ? 0.f : M) + __log2f(Lsum)) * LN2;
+    };
+    float M, Lsum, v[2];
+    // the CTA's own part replaces warp 0's O; its maxima and sums lie behind it
+    constexpr int O_AT = 8 * L::ROWS, ML_AT = O_AT + 4 * L::ROWS * DV;
+    for (int e = threadIdx.x; e < rows * (DV / 2); e += THREADS) {
+        const int row = e / (DV / 2), c = e % (DV / 2) * 2;
+        auto at_warp = [&](int w) { return smem + w * L::STAGES * L::BYTES_BLOCK; };
+        merge(std::integral_constant<int, WARPS>{},
+              [&](int w) { return *reinterpret_cast<const float2*>(at_warp(w) + 8 * row); },
+              [&](int w) { return *reinterpret_cast<const float2*>(at_warp(w) + O_AT + 4 * (row * DV + c)); }, &M, &Lsum, v);
+        if (p.cluster == 1) {
+            write(row, c, M, Lsum, v);
+        } else {
+            *reinterpret_cast<float2*>(smem + O_AT + 4 * (row * DV + c)) = make_float2(v[0], v[1]);
+            if (c == 0) *reinterpret_cast<float2*>(smem + ML_AT + 8 * row) = make_float2(M, Lsum);
+        }
     }
+    if (p.cluster == 1) return;
+    cluster_sync();
+    const uint32_t base = smem_u32(smem);
+    for (int e = (static_cast<int>(blockIdx.x) % p.cluster) * THREADS + threadIdx.x; e < rows * (DV / 2); e += THREADS * p.cluster) {
+        const int row = e / (DV / 2), c = e % (DV / 2) * 2;
+        auto ml = [&](int k) { return k < p.cluster ? load_cluster(base + ML_AT + 8 * row, k) : make_float2(-INFINITY, 0.f); };
+        auto o = [&](int k) { return k < p.cluster ? load_cluster(base + O_AT + 4 * (row * DV + c), k) : make_float2(0.f, 0.f); };
+        merge(std::integral_constant<int, MAX_CLUSTER>{}, ml, o, &M, &Lsum, v);
+        write(row, c, M, Lsum, v);
+    }
+    cluster_sync();                                      // the others may still read this CTA's part
 }
 
 // Merge of the parts of the cut pairs, p.merge_warps warps to each (pair, row): slot 1 of
@@ -976,10 +1012,11 @@ cudaError_t launch(const DecodeQ4Params& p, cudaStream_t stream)
         if (e != cudaSuccess) return e;
         configured[dev] = true;
     }
-    const unsigned ctas = CTA ? static_cast<unsigned>(p.B) * p.H_kv * p.row_tiles
-                              : static_cast<unsigned>((p.warps + WARPS - 1) / WARPS);
-    e = launch_pdl(kern, dim3(ctas), dim3(THREADS), L::BYTES, stream, p);
-    if (e != cudaSuccess || CTA || p.mode != Q4_SHARES) return e;
+    if (CTA)
+        return launch_pdl_cluster(kern, p.cluster, dim3(static_cast<unsigned>(p.B) * p.H_kv * p.row_tiles * p.cluster),
+                                  dim3(THREADS), L::BYTES, stream, p);
+    e = launch_pdl(kern, dim3(static_cast<unsigned>((p.warps + WARPS - 1) / WARPS)), dim3(THREADS), L::BYTES, stream, p);
+    if (e != cudaSuccess || p.mode != Q4_SHARES) return e;
     const int64_t items = static_cast<int64_t>(p.B) * p.H_kv * p.row_tiles * p.part_rows;
     const int per = MERGE_WARPS / p.merge_warps;
     return launch_pdl(attn_decode_q4_merge_kernel<DV>, dim3(static_cast<unsigned>((items + per - 1) / per)),
