@@ -399,47 +399,31 @@ def merge_proj(O: torch.Tensor, W_o: torch.Tensor, bias: torch.Tensor | None = N
     return Y
 
 
-class _Here:
-    """The current device's current stream, as a context."""
-    __slots__ = ("handle",)
-
-    def __init__(self, handle):
-        self.handle = handle
-
-    def __enter__(self):
-        return self.handle
-
-    def __exit__(self, *exc):
-        return None
-
-
 @contextlib.contextmanager
 def _there(device, stream):
+    """Make ``device`` and ``stream`` (a torch stream, a cudaStream_t as an int, or None for the
+    device's current stream) the current ones. What is allocated inside belongs to that
+    stream, so that its memory is not handed on while a kernel there still uses it."""
     with torch.cuda.device(device):
         if stream is None:
-            yield int(torch.cuda.current_stream().cuda_stream)
+            yield
             return
         if not hasattr(stream, "cuda_stream"):
             stream = torch.cuda.ExternalStream(int(stream), device=device)
         with torch.cuda.stream(stream):
-            yield int(stream.cuda_stream)
+            yield
 
 
-def _on(device, stream):
-    """Run on ``device`` and ``stream`` (a torch stream, a cudaStream_t as an int, or None
-    for the device's current stream); yields the stream's handle. What is allocated
-    inside belongs to that stream, so that its memory is not handed on while a kernel
-    there still uses it. (The ordinary case, the current device and stream, switches
-    nothing: torch's own context managers take 5 us of the host's time, twice a short call's.)"""
-    if stream is None and device.index == torch.cuda.current_device():
-        return _Here(torch._C._cuda_getCurrentRawStream(device.index))
-    return _there(device, stream)
+# A short call on the 4-bit cache is bound by the host: its functions look at each tensor once, by
+# the cheapest attribute, and switch device or stream (5 us) only where they have to.
+_current_device = getattr(torch._C, "_cuda_getDevice", None)               # (None without CUDA)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _cuda_arg(name, t, dtype, shape, device):
-    """Check an argument (``shape`` as a tuple) that must lie contiguous on ``device``."""
-    if t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {device}")
+def _cuda_arg(name, t, dtype, shape, gpu):
+    """Check an argument (``shape`` as a tuple) that must lie contiguous on the device of index ``gpu``."""
+    if t.dtype is not dtype or t.get_device() != gpu or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on cuda:{gpu}")
 
 
 def cache_q4_empty(B: int, H_kv: int, m: int, d_k: int, d_v: int, device="cuda") -> torch.Tensor:
@@ -449,17 +433,19 @@ def cache_q4_empty(B: int, H_kv: int, m: int, d_k: int, d_v: int, device="cuda")
 
 
 def _cache_q4_dims(cache, d_k, m):
-    """Check the cache tensor; (B, H_kv, m, d_v) with ``m`` slots (None: all of its blocks')."""
-    if cache.dtype != torch.uint8 or not cache.is_cuda or cache.dim() != 4 or not cache.is_contiguous() \
-            or cache.shape[3] % 34 != 0:
+    """Check the cache tensor; (B, H_kv, m, d_v, device index) with ``m`` slots (None: all of its blocks')."""
+    if cache.dtype is not torch.uint8 or not cache.is_cuda or cache.dim() != 4 or not cache.is_contiguous():
         raise ValueError("cache must be a contiguous uint8 CUDA tensor [B, H_kv, blocks, 34 (d_k + d_v)]")
     B, H_kv, blocks, width = cache.shape
+    width, rest = divmod(width, 34)
+    if rest:
+        raise ValueError("cache must be a contiguous uint8 CUDA tensor [B, H_kv, blocks, 34 (d_k + d_v)]")
     m = blocks * CACHE_Q4_BLOCK if m is None else int(m)
     if m < 0 or -(-m // CACHE_Q4_BLOCK) != blocks:
         raise ValueError(f"a cache of {m} slots has {-(-m // CACHE_Q4_BLOCK)} blocks, not {blocks}")
-    if not 0 < d_k < width // 34:
-        raise ValueError(f"the cache's rows are {width // 34} channels wide in all: no room for d_k = {d_k} and a d_v")
-    return B, H_kv, m, width // 34 - d_k
+    if not 0 < d_k < width:
+        raise ValueError(f"the cache's rows are {width} channels wide in all: no room for d_k = {d_k} and a d_v")
+    return B, H_kv, m, width - d_k, cache.get_device()
 
 
 def cache_q4_write(cache: torch.Tensor, K: torch.Tensor, V: torch.Tensor, starts: torch.Tensor | None = None,
@@ -472,19 +458,22 @@ def cache_q4_write(cache: torch.Tensor, K: torch.Tensor, V: torch.Tensor, starts
     _bf16_cuda("V", V, 4)
     B, H_kv, n, d_k = K.shape
     d_v = V.shape[3]
-    cB, cH, m, c_dv = _cache_q4_dims(cache, d_k, m)
-    if tuple(V.shape[:3]) != (B, H_kv, n) or (cB, cH, c_dv) != (B, H_kv, d_v):
+    cB, cH, m, c_dv, gpu = _cache_q4_dims(cache, d_k, m)
+    if V.shape != (B, H_kv, n, d_v) or cB != B or cH != H_kv or c_dv != d_v:
         raise ValueError("inconsistent K/V/cache shapes")
-    dev = cache.device
-    if K.device != dev or V.device != dev:
+    if K.get_device() != gpu or V.get_device() != gpu:
         raise ValueError("K, V and the cache must be on one device")
-    for name, t in (("starts", starts), ("counts", counts)):
-        if t is not None:
-            _cuda_arg(name, t, torch.int32, (B,), dev)
-    with _on(dev, stream) as handle:
-        rc = load().attn_cache_q4_write(K.data_ptr(), V.data_ptr(), B, H_kv, n, m, d_k, d_v,
-                                        None if starts is None else starts.data_ptr(),
-                                        None if counts is None else counts.data_ptr(), cache.data_ptr(), handle)
+    if starts is not None:
+        _cuda_arg("starts", starts, torch.int32, (B,), gpu)
+    if counts is not None:
+        _cuda_arg("counts", counts, torch.int32, (B,), gpu)
+    if stream is not None or gpu != _current_device():
+        with _there(gpu, stream):
+            return cache_q4_write(cache, K, V, starts, counts, m)
+    rc = load().attn_cache_q4_write(K.data_ptr(), V.data_ptr(), B, H_kv, n, m, d_k, d_v,
+                                    None if starts is None else starts.data_ptr(),
+                                    None if counts is None else counts.data_ptr(), cache.data_ptr(),
+                                    _current_stream(gpu))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_cache_q4_write", last_error() if rc == ATTN_ERR_CUDA else "")
     return cache
@@ -497,23 +486,26 @@ def cache_q4_read(cache: torch.Tensor, d_k: int, m: int | None = None, key_lengt
     (K [B,H,n,d_k], V [B,H,n,d_v]), exactly the values held; each cache head is copied to
     its H / H_kv query heads (``H`` defaults to H_kv). Slots at or past ``key_lengths[b]``
     (int32 CUDA [B]) give 0. Asynchronous on ``stream``."""
-    B, H_kv, m, d_v = _cache_q4_dims(cache, d_k, m)
+    B, H_kv, m, d_v, gpu = _cache_q4_dims(cache, d_k, m)
     H = H_kv if H is None else int(H)
     n = m - first if n is None else int(n)
-    dev = cache.device
     if first < 0 or n < 0 or first + n > m or H < 0 or (H % H_kv if H_kv else H):
         raise ValueError("slots outside the cache, or H not a multiple of its heads")
     if key_lengths is not None:
-        _cuda_arg("key_lengths", key_lengths, torch.int32, (B,), dev)
-    for name, t, d in (("K", K, d_k), ("V", V, d_v)):
-        if t is not None:
-            _cuda_arg(name, t, torch.bfloat16, (B, H, n, d), dev)
-    with _on(dev, stream) as handle:
-        K = torch.empty((B, H, n, d_k), dtype=torch.bfloat16, device=dev) if K is None else K
-        V = torch.empty((B, H, n, d_v), dtype=torch.bfloat16, device=dev) if V is None else V
-        rc = load().attn_cache_q4_read(cache.data_ptr(), B, H, H_kv, m, int(first), n, d_k, d_v,
-                                       None if key_lengths is None else key_lengths.data_ptr(), K.data_ptr(),
-                                       V.data_ptr(), handle)
+        _cuda_arg("key_lengths", key_lengths, torch.int32, (B,), gpu)
+    if K is not None:
+        _cuda_arg("K", K, torch.bfloat16, (B, H, n, d_k), gpu)
+    if V is not None:
+        _cuda_arg("V", V, torch.bfloat16, (B, H, n, d_v), gpu)
+    if stream is not None or gpu != _current_device():
+        with _there(gpu, stream):
+            return cache_q4_read(cache, d_k, m, key_lengths, H, first, n, K, V)
+    dev = cache.device
+    K = torch.empty((B, H, n, d_k), dtype=torch.bfloat16, device=dev) if K is None else K
+    V = torch.empty((B, H, n, d_v), dtype=torch.bfloat16, device=dev) if V is None else V
+    rc = load().attn_cache_q4_read(cache.data_ptr(), B, H, H_kv, m, int(first), n, d_k, d_v,
+                                   None if key_lengths is None else key_lengths.data_ptr(), K.data_ptr(),
+                                   V.data_ptr(), _current_stream(gpu))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_cache_q4_read", last_error() if rc == ATTN_ERR_CUDA else "")
     return K, V
@@ -538,38 +530,41 @@ def decode_q4(Q: torch.Tensor, cache: torch.Tensor, mask: str = "none", key_leng
         raise ValueError(f"unknown mask {mask!r}")
     _bf16_cuda("Q", Q, 4)
     B, H, n, d_k = Q.shape
-    cB, H_kv, m, d_v = _cache_q4_dims(cache, d_k, m)
-    dev = cache.device
-    if cB != B or Q.device != dev or (H % H_kv if H_kv else H):
+    cB, H_kv, m, d_v, gpu = _cache_q4_dims(cache, d_k, m)
+    if cB != B or Q.get_device() != gpu or (H % H_kv if H_kv else H):
         raise ValueError("Q and the cache must have the same batch and device, and H be a multiple of the cache's heads")
     uses_lengths = mask in _inputs.LENGTH_MASKS
     if uses_lengths:
         if key_lengths is None:
             raise ValueError(f"{mask} needs key_lengths: contiguous int32 CUDA [B]")
-        _cuda_arg("key_lengths", key_lengths, torch.int32, (B,), dev)
+        _cuda_arg("key_lengths", key_lengths, torch.int32, (B,), gpu)
     if slopes is not None:
-        _cuda_arg("slopes", slopes, torch.float32, (H,), dev)
+        _cuda_arg("slopes", slopes, torch.float32, (H,), gpu)
     if O is not None:
-        _cuda_arg("O", O, torch.bfloat16, (B, H, n, d_v), dev)
+        _cuda_arg("O", O, torch.bfloat16, (B, H, n, d_v), gpu)
     if LSE is not None:
-        _cuda_arg("LSE", LSE, torch.float32, (B, H, n), dev)
+        _cuda_arg("LSE", LSE, torch.float32, (B, H, n), gpu)
     ws_bytes = decode_q4_workspace_size(B, H, H_kv, n, m, d_k, d_v)
-    if workspace is not None and (workspace.dtype != torch.uint8 or workspace.device != dev
+    if workspace is not None and (workspace.dtype is not torch.uint8 or workspace.get_device() != gpu
                                   or workspace.numel() < ws_bytes or not workspace.is_contiguous()):
-        raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {ws_bytes} bytes on {dev}")
-    with _on(dev, stream) as handle:
-        O = torch.empty((B, H, n, d_v), dtype=torch.bfloat16, device=dev) if O is None else O
-        if LSE is None and want_lse:
-            LSE = torch.empty((B, H, n), dtype=torch.float32, device=dev)
-        if workspace is None and ws_bytes > 0:
-            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-        rc = load().attn_decode_q4(Q.data_ptr(), cache.data_ptr(), B, H, H_kv, n, m, d_k, d_v, MASK_CODES[mask],
-                                   key_lengths.data_ptr() if uses_lengths else None,
-                                   None if slopes is None else slopes.data_ptr(),
-                                   -1.0 if scale is None else float(scale), O.data_ptr(),
-                                   None if LSE is None else LSE.data_ptr(),
-                                   None if workspace is None else workspace.data_ptr(),
-                                   0 if workspace is None else workspace.numel(), handle)
+        raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {ws_bytes} bytes on cuda:{gpu}")
+    if stream is not None or gpu != _current_device():
+        with _there(gpu, stream):
+            return decode_q4(Q, cache, mask, key_lengths, scale, m, slopes, O, LSE, want_lse, workspace)
+    dev = cache.device
+    if O is None:
+        O = torch.empty((B, H, n, d_v), dtype=torch.bfloat16, device=dev)
+    if LSE is None and want_lse:
+        LSE = torch.empty((B, H, n), dtype=torch.float32, device=dev)
+    if workspace is None and ws_bytes > 0:
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    rc = load().attn_decode_q4(Q.data_ptr(), cache.data_ptr(), B, H, H_kv, n, m, d_k, d_v, MASK_CODES[mask],
+                               key_lengths.data_ptr() if uses_lengths else None,
+                               None if slopes is None else slopes.data_ptr(),
+                               -1.0 if scale is None else float(scale), O.data_ptr(),
+                               None if LSE is None else LSE.data_ptr(),
+                               None if workspace is None else workspace.data_ptr(),
+                               0 if workspace is None else workspace.numel(), _current_stream(gpu))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_decode_q4", last_error() if rc == ATTN_ERR_CUDA else "")
     return O, LSE

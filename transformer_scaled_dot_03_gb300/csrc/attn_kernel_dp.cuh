@@ -131,7 +131,7 @@ struct Unit {
 //
 // SHARED is the instantiation for K and V whose heads groups of query heads share
 // (p.kv_group; the 4-bit cache read back): its callers have few query tiles against many
-// keys, so its units are single tiles under every mask (4 x 16 heads, 256 rows at the end of up
+// keys, so its units are single tiles under every mask (4 x 16 heads, 256 rows at the end of
 // up to 4096 slots: 29 us, 59 in pairs, which occupy 64 CTAs). Told apart by a template, since
 // a choice at run time cost the plain causal kernels 0.7 to 4%.
 //
