@@ -72,6 +72,14 @@ __device__ __forceinline__ float rint_ratio(float x, float r)
     return __fadd_rn(__fmaf_rn(x, r, c), RINT - c);
 }
 
+// The same of both channels of a word, by packed instructions: two issue slots instead of four
+// (prompts and read back 34.2 -> 33.7 us).
+__device__ __forceinline__ uint64_t rint_ratio2(uint32_t pair, float r)
+{
+    const uint64_t x = f2_pack(__uint_as_float(pair << 16), __uint_as_float(pair & 0xFFFF0000u));
+    return f2_add(f2_fma(x, f2_pack(r, r), f2_pack(6144.f, 6144.f)), f2_pack(RINT - 6144.f, RINT - 6144.f));
+}
+
 // One lane of four quantises channels 16 t .. 16 t + 15 of a group (t = lane % 4): the
 // codes as 16 nibbles, and the group's word (the same in all four lanes).
 __device__ __forceinline__ uint2 quantise(const uint32_t (&w)[8], uint32_t* word)
@@ -109,25 +117,27 @@ __device__ __forceinline__ uint2 quantise(const uint32_t (&w)[8], uint32_t* word
         // rint(x / s) + u0 is in 0..15 (rint is odd and monotone, |x| <= hi or neg), except
         // that two exact halves at the ends may add up to 16
         // the rounded sums' bits times 16^i, modulo 2^32
-        auto encode = [&](auto&& rounded) {
+        auto encode = [&](auto&& capped) {
             uint32_t c[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint32_t sum = 0u;
 #pragma unroll
-                for (int i = 7; i >= 0; --i) {
-                    const uint32_t pair = w[4 * h + i / 2];
-                    sum = sum * 16u + __float_as_uint(rounded(__uint_as_float(i % 2 ? pair & 0xFFFF0000u : pair << 16)));
+                for (int i = 3; i >= 0; --i) {
+                    float even, odd;
+                    f2_unpack(rint_ratio2(w[4 * h + i], r), even, odd);
+                    sum = sum * 16u + __float_as_uint(capped(odd));
+                    sum = sum * 16u + __float_as_uint(capped(even));
                 }
                 c[h] = sum - (RINT_BITS - u0) * 0x11111111u;
             }
             return make_uint2(c[0], c[1]);
         };
         if (__float_as_uint(rint_ratio(hi, r)) - RINT_BITS + u0 <= 15u) {
-            codes = encode([&](float x) { return rint_ratio(x, r); });
+            codes = encode([](float x) { return x; });
         } else {
             const float most = RINT + 15.f - static_cast<float>(u0);
-            codes = encode([&](float x) { return fminf(rint_ratio(x, r), most); });
+            codes = encode([&](float x) { return fminf(x, most); });
         }
     } else {
         sb = (__float_as_uint(__fdiv_rn(range, 15.f)) + 0xFFFFFu) & 0xFFF00000u;
